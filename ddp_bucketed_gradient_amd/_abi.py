@@ -14,9 +14,14 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 HIP_LIB = os.path.join(_HERE, "lib", "libddpb.so")
 HOSTONLY_LIB = os.path.join(_HERE, "lib", "libddpb_hostonly.so")
 
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 MODE_FUSED, MODE_STAGED = 0, 1
 BIND_DEVICE_TIMESTAMPS, BIND_TIME_LAUNCHES, BIND_ROCTX, BIND_OVERLAP = 1, 2, 4, 8
+
+NORM_SKIP_NONFINITE = 1
+STATE_F32, STATE_F8 = 0, 1
+STATE_BLOCK = 64                     # DDPB_STATE_BLOCK: elements that share one 8-bit scale
+ADAMW_MASTER = 1
 
 STATIC_SCRATCH_BYTES = 32 << 20      # DDPB_STATIC_SCRATCH_BYTES
 
@@ -34,6 +39,9 @@ SYMBOLS = [
     "ddpb_set_workgroups_per_cu", "ddpb_set_sync_step",
     "ddpb_view_storage_elems", "ddpb_get_view_offset", "ddpb_bind_bucket_views",
     "ddpb_rebuild_buckets", "ddpb_get_ready_order", "ddpb_set_local_used", "ddpb_bind_static",
+    "ddpb_norm_create", "ddpb_norm_destroy", "ddpb_norm_workspace_bytes", "ddpb_norm_bind", "ddpb_norm_compute",
+    "ddpb_adamw_create", "ddpb_adamw_destroy", "ddpb_adamw_workspace_bytes", "ddpb_adamw_bind", "ddpb_adamw_step",
+    "ddpb_adamw_set_step", "ddpb_adamw_get_step",
 ]
 
 
@@ -43,7 +51,8 @@ class DdpbError(RuntimeError):
         self.code = code
 
 
-i32, i64, vp = C.c_int32, C.c_int64, C.c_void_p
+i32, i64, vp, f64 = C.c_int32, C.c_int64, C.c_void_p, C.c_double
+PF64 = C.POINTER(C.c_double)
 P32, P64 = C.POINTER(C.c_int32), C.POINTER(C.c_int64)
 
 
@@ -84,12 +93,25 @@ def _sig(lib):
         "ddpb_view_storage_elems": [vp, P64],
         "ddpb_get_view_offset": [vp, i32, P64],
         "ddpb_bind_bucket_views": [vp, C.POINTER(vp), i64, vp, C.POINTER(vp), i32, i32],
+        "ddpb_norm_create": [P64, P32, i32, C.POINTER(vp)],
+        "ddpb_norm_destroy": [vp],
+        "ddpb_norm_workspace_bytes": [vp, P64],
+        "ddpb_norm_bind": [vp, C.POINTER(vp), vp, i64, vp, vp],
+        "ddpb_norm_compute": [vp, vp, f64, f64, i32],
+        "ddpb_adamw_create": [P64, i32, i32, i32, i32, i32, i32, f64, f64, f64, PF64, PF64, C.c_uint64,
+                              C.POINTER(vp)],
+        "ddpb_adamw_destroy": [vp],
+        "ddpb_adamw_workspace_bytes": [vp, P64],
+        "ddpb_adamw_bind": [vp] + [C.POINTER(vp)] * 7 + [i64, vp, i64, vp, vp],
+        "ddpb_adamw_step": [vp, vp, f64, vp, f64, vp],
+        "ddpb_adamw_set_step": [vp, i64],
+        "ddpb_adamw_get_step": [vp, P64],
         "ddpb_last_error": [],
     }
     for name, args in S.items():
         f = getattr(lib, name)
         f.argtypes = args
-        f.restype = None if name == "ddpb_destroy" else (C.c_char_p if name == "ddpb_last_error" else C.c_int)
+        f.restype = None if name.endswith("_destroy") else (C.c_char_p if name == "ddpb_last_error" else C.c_int)
 
 
 class Lib:
@@ -206,6 +228,72 @@ class Lib:
 
     def reset(self, h):
         self._check(self.dll.ddpb_reset(h))
+
+    # -- after the synchronisation ------------------------------------------------------
+    def norm_create(self, numel: Sequence[int], dtypes: Sequence[int]):
+        h = vp()
+        self._check(self.dll.ddpb_norm_create((C.c_int64 * max(len(numel), 1))(*numel),
+                                              (C.c_int32 * max(len(dtypes), 1))(*dtypes), len(numel), C.byref(h)))
+        return h
+
+    def norm_destroy(self, n):
+        self.dll.ddpb_norm_destroy(n)
+
+    def norm_workspace_bytes(self, n) -> int:
+        b = i64()
+        self._check(self.dll.ddpb_norm_workspace_bytes(n, C.byref(b)))
+        return b.value
+
+    def norm_bind(self, n, grads: Sequence[int], workspace: int, ws_bytes: int, stream: int, reducer=None):
+        self._check(self.dll.ddpb_norm_bind(n, ptr_array(grads), workspace or None, int(ws_bytes), stream or None,
+                                            reducer))
+
+    def norm_compute(self, n, max_norm: float, grad_scale: float = 1.0, flags: int = 0, reducer=None):
+        rc = self.dll.ddpb_norm_compute(n, reducer, max_norm, grad_scale, flags)
+        if rc != OK:
+            raise DdpbError(rc, self.last_error())
+
+    def adamw_create(self, numel: Sequence[int], R: int, param_dtype: int, grad_dtype: int, state: int, flags: int,
+                     beta1: float, beta2: float, eps: float, weight_decay: Optional[Sequence[float]] = None,
+                     lr_scale: Optional[Sequence[float]] = None, seed: int = 0):
+        h, n = vp(), len(numel)
+        if any(x is not None and len(x) != n for x in (weight_decay, lr_scale)):
+            raise ValueError("weight_decay and lr_scale need one value for each variable")
+        wd, ls = ((C.c_double * max(n, 1))(*x) if x is not None else None for x in (weight_decay, lr_scale))
+        self._check(self.dll.ddpb_adamw_create((C.c_int64 * max(n, 1))(*numel), n, int(R), param_dtype, grad_dtype,
+                                               state, flags, beta1, beta2, eps, wd, ls,
+                                               int(seed) & 0xFFFFFFFFFFFFFFFF, C.byref(h)))
+        return h
+
+    def adamw_destroy(self, a):
+        self.dll.ddpb_adamw_destroy(a)
+
+    def adamw_workspace_bytes(self, a) -> int:
+        b = i64()
+        self._check(self.dll.ddpb_adamw_workspace_bytes(a, C.byref(b)))
+        return b.value
+
+    def adamw_bind(self, a, params: Sequence[int], grads: Sequence[int], master: Optional[Sequence[int]],
+                   exp_avg: Sequence[int], second: Sequence[int], avg_scale: Optional[Sequence[int]],
+                   root_scale: Optional[Sequence[int]], step: int, workspace: int, ws_bytes: int, stream: int,
+                   reducer=None):
+        arr = [ptr_array(x) if x is not None else None
+               for x in (params, grads, master, exp_avg, second, avg_scale, root_scale)]
+        self._check(self.dll.ddpb_adamw_bind(a, *arr, int(step), workspace or None, int(ws_bytes), stream or None,
+                                             reducer))
+
+    def adamw_step(self, a, lr: float, lr_device: int = 0, grad_scale: float = 1.0, clip: int = 0, reducer=None):
+        rc = self.dll.ddpb_adamw_step(a, reducer, lr, lr_device or None, grad_scale, clip or None)
+        if rc != OK:
+            raise DdpbError(rc, self.last_error())
+
+    def adamw_set_step(self, a, step: int):
+        self._check(self.dll.ddpb_adamw_set_step(a, int(step)))
+
+    def adamw_get_step(self, a) -> int:
+        t = i64()
+        self._check(self.dll.ddpb_adamw_get_step(a, C.byref(t)))
+        return t.value
 
     # -- diagnostics ------------------------------------------------------------------
     def get_launch_log(self, h, with_stamps: bool = False):

@@ -26,7 +26,7 @@ HIP_LIB = os.path.join(LIBDIR, "libddpb.so")
 HOST_LIB = os.path.join(LIBDIR, "libddpb_hostonly.so")
 ARCH = "gfx950"
 
-HOST_SOURCES = ["plan.cpp", "core.cpp", "abi.cpp"]
+HOST_SOURCES = ["plan.cpp", "core.cpp", "optim.cpp", "abi.cpp"]
 
 # -ffp-contract=off: no fused multiply-add may change the rounding of the mean.
 # packed-fp32-ops disabled: the float4 adds stay scalar v_add_f32.
@@ -50,7 +50,7 @@ def _run(cmd):
 
 def build_hip(out: str = HIP_LIB) -> str:
     os.makedirs(os.path.dirname(out), exist_ok=True)
-    srcs = [os.path.join(CSRC, s) for s in HOST_SOURCES + ["kernels.hip"]]
+    srcs = [os.path.join(CSRC, s) for s in HOST_SOURCES + ["kernels.hip", "optim.hip"]]
     tmp = out + ".tmp"
     _run([_hipcc()] + HIPCC_FLAGS + srcs + ["-L/opt/rocm/lib", "-lrocprofiler-sdk-roctx", "-o", tmp])
     os.replace(tmp, out)

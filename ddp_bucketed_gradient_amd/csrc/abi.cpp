@@ -2,6 +2,7 @@
 // checking and marshalling only; the work happens in plan.cpp, core.cpp and the
 // launcher.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <new>
 #include <string>
@@ -9,10 +10,22 @@
 
 #include "../../include/ddpb.h"
 #include "core.hpp"
+#include "optim.hpp"
 
 struct ddpb_reducer {
   explicit ddpb_reducer(ddpb::Plan p) : red(std::move(p)) {}
   ddpb::Reducer red;
+};
+
+struct ddpb_norm {
+  ddpb_norm(std::vector<int64_t> numel, std::vector<int32_t> dtypes) : norm(std::move(numel), std::move(dtypes)) {}
+  ddpb::Norm norm;
+  int32_t P = 0;
+};
+
+struct ddpb_adamw {
+  explicit ddpb_adamw(ddpb::AdamwConfig c) : opt(std::move(c)) {}
+  ddpb::Adamw opt;
 };
 
 namespace {
@@ -26,6 +39,31 @@ int fail(int code, const std::string& msg) {
 int pass(int code, const std::string& msg) {
   if (code != 0) g_err = msg;
   return code;
+}
+
+bool is_dtype(int32_t d) { return d == DDPB_F32 || d == DDPB_BF16 || d == DDPB_F16; }
+
+const ddpb::Reducer* reducer_of(ddpb_t h) { return h != nullptr ? &h->red : nullptr; }
+
+// Element counts whose tables and addresses stay in range.
+bool numels_ok(const int64_t* numel, int32_t P) {
+  int64_t total = 0;
+  for (int32_t v = 0; v < P; ++v) {
+    if (numel[v] < 0 || numel[v] > (int64_t(1) << 40) || (total += numel[v]) > (int64_t(1) << 40)) return false;
+  }
+  return true;
+}
+
+// A call that may allocate host memory: no C++ exception crosses the ABI.
+template <typename F>
+int guarded(const char* what, F f) {
+  try {
+    std::string err;
+    const int rc = f(&err);
+    return rc == DDPB_OK ? rc : fail(rc, err);
+  } catch (const std::exception&) {
+    return fail(DDPB_E_NOMEM, std::string(what) + ": out of host memory");
+  }
 }
 }  // namespace
 
@@ -351,6 +389,127 @@ int ddpb_device_clock_hz(ddpb_t h, int64_t* hz) {
   if (!h || !hz) return fail(DDPB_E_ARG, "device_clock_hz: NULL argument");
   std::string err;
   return pass(h->red.launcher()->clock_hz(hz, &err), err);
+}
+
+int ddpb_norm_create(const int64_t* numel, const int32_t* dtypes, int32_t P, ddpb_norm_t* out) {
+  if (out == nullptr) return fail(DDPB_E_ARG, "norm create: out is NULL");
+  *out = nullptr;
+  if (P < 0 || (P > 0 && (numel == nullptr || dtypes == nullptr)))
+    return fail(DDPB_E_ARG, "norm create: bad P, numel or dtypes");
+  if (!numels_ok(numel, P)) return fail(DDPB_E_ARG, "norm create: bad numel");
+  for (int32_t v = 0; v < P; ++v)
+    if (!is_dtype(dtypes[v])) return fail(DDPB_E_ARG, "norm create: bad dtype");
+  return guarded("norm create", [&](std::string*) {
+    *out = new ddpb_norm(std::vector<int64_t>(numel, numel + P), std::vector<int32_t>(dtypes, dtypes + P));
+    (*out)->P = P;
+    return DDPB_OK;
+  });
+}
+
+void ddpb_norm_destroy(ddpb_norm_t n) { delete n; }
+
+int ddpb_norm_workspace_bytes(ddpb_norm_t n, int64_t* bytes) {
+  if (!n || !bytes) return fail(DDPB_E_ARG, "norm workspace_bytes: NULL argument");
+  *bytes = n->norm.workspace_bytes();
+  return DDPB_OK;
+}
+
+int ddpb_norm_bind(ddpb_norm_t n, void* const* grads, void* workspace, int64_t ws_bytes, void* stream, ddpb_t h) {
+  if (!n) return fail(DDPB_E_ARG, "norm bind: NULL handle");
+  if (n->P > 0 && grads == nullptr) return fail(DDPB_E_ARG, "norm bind: grads is NULL");
+  return guarded("norm bind", [&](std::string* err) {
+    return n->norm.bind(grads, workspace, ws_bytes, stream, reducer_of(h), err);
+  });
+}
+
+int ddpb_norm_compute(ddpb_norm_t n, ddpb_t h, double max_norm, double grad_scale, int32_t flags) {
+  if (!n) return fail(DDPB_E_ARG, "norm compute: NULL handle");
+  if (flags & ~DDPB_NORM_SKIP_NONFINITE) return fail(DDPB_E_ARG, "norm compute: bad flags");
+  return guarded("norm compute", [&](std::string* err) {
+    return n->norm.compute(reducer_of(h), max_norm, grad_scale, (flags & DDPB_NORM_SKIP_NONFINITE) != 0, err);
+  });
+}
+
+int ddpb_adamw_create(const int64_t* numel, int32_t P, int32_t R, int32_t param_dtype, int32_t grad_dtype,
+                      int32_t state, int32_t flags, double beta1, double beta2, double eps,
+                      const double* weight_decay, const double* lr_scale, uint64_t seed, ddpb_adamw_t* out) {
+  if (out == nullptr) return fail(DDPB_E_ARG, "adamw create: out is NULL");
+  *out = nullptr;
+  if (P < 0 || (P > 0 && numel == nullptr) || !numels_ok(numel, P))
+    return fail(DDPB_E_ARG, "adamw create: bad P or numel");
+  if (R < 1 || R > ddpb::kMaxReplicas) return fail(DDPB_E_ARG, "adamw create: R must be in 1..64");
+  if (!is_dtype(param_dtype) || !is_dtype(grad_dtype)) return fail(DDPB_E_ARG, "adamw create: bad dtype");
+  if (state != DDPB_STATE_F32 && state != DDPB_STATE_F8) return fail(DDPB_E_ARG, "adamw create: bad state type");
+  if (flags & ~DDPB_ADAMW_MASTER) return fail(DDPB_E_ARG, "adamw create: bad flags");
+  if ((flags & DDPB_ADAMW_MASTER) && param_dtype == DDPB_F32)
+    return fail(DDPB_E_ARG, "adamw create: fp32 parameters take no master copy");
+  if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) || !std::isfinite(eps))
+    return fail(DDPB_E_ARG, "adamw create: betas must be in [0, 1), eps finite and not negative");
+  for (int32_t v = 0; v < P; ++v) {
+    if (weight_decay != nullptr && !(weight_decay[v] >= 0 && std::isfinite(weight_decay[v])))
+      return fail(DDPB_E_ARG, "adamw create: weight_decay must be finite and not negative");
+    if (lr_scale != nullptr && !(lr_scale[v] >= 0 && std::isfinite(lr_scale[v])))
+      return fail(DDPB_E_ARG, "adamw create: lr_scale must be finite and not negative");
+  }
+  return guarded("adamw create", [&](std::string*) {
+    ddpb::AdamwConfig c;
+    c.numel.assign(numel, numel + P);
+    c.R = R;
+    c.param_dtype = param_dtype;
+    c.grad_dtype = grad_dtype;
+    c.f8 = state == DDPB_STATE_F8;
+    c.master = (flags & DDPB_ADAMW_MASTER) != 0;
+    c.beta1 = beta1;
+    c.beta2 = beta2;
+    c.eps = eps;
+    if (weight_decay != nullptr) c.weight_decay.assign(weight_decay, weight_decay + P);
+    if (lr_scale != nullptr) c.lr_scale.assign(lr_scale, lr_scale + P);
+    c.seed = seed;
+    *out = new ddpb_adamw(std::move(c));
+    return DDPB_OK;
+  });
+}
+
+void ddpb_adamw_destroy(ddpb_adamw_t a) { delete a; }
+
+int ddpb_adamw_workspace_bytes(ddpb_adamw_t a, int64_t* bytes) {
+  if (!a || !bytes) return fail(DDPB_E_ARG, "adamw workspace_bytes: NULL argument");
+  *bytes = a->opt.workspace_bytes();
+  return DDPB_OK;
+}
+
+int ddpb_adamw_bind(ddpb_adamw_t a, void* const* params, void* const* grads, void* const* master,
+                    void* const* exp_avg, void* const* second, void* const* avg_scale, void* const* root_scale,
+                    int64_t step, void* workspace, int64_t ws_bytes, void* stream, ddpb_t h) {
+  if (!a) return fail(DDPB_E_ARG, "adamw bind: NULL handle");
+  const ddpb::AdamwConfig& c = a->opt.config();
+  if (!c.numel.empty()) {
+    if (!params || !grads || !exp_avg || !second) return fail(DDPB_E_ARG, "adamw bind: NULL pointer array");
+    if (c.master && !master) return fail(DDPB_E_ARG, "adamw bind: master is NULL");
+    if (c.f8 && (!avg_scale || !root_scale)) return fail(DDPB_E_ARG, "adamw bind: 8-bit states need their scales");
+  }
+  const ddpb::AdamwBuffers b{params, grads, master, exp_avg, second, avg_scale, root_scale};
+  return guarded("adamw bind", [&](std::string* err) {
+    return a->opt.bind(b, step, workspace, ws_bytes, stream, reducer_of(h), err);
+  });
+}
+
+int ddpb_adamw_step(ddpb_adamw_t a, ddpb_t h, double lr, const float* lr_device, double grad_scale,
+                    const void* clip) {
+  if (!a) return fail(DDPB_E_ARG, "adamw step: NULL handle");
+  return guarded("adamw step", [&](std::string* err) {
+    return a->opt.step(reducer_of(h), lr, lr_device, grad_scale, clip, err);
+  });
+}
+
+int ddpb_adamw_set_step(ddpb_adamw_t a, int64_t step) {
+  if (!a) return fail(DDPB_E_ARG, "adamw set_step: NULL handle");
+  return guarded("adamw set_step", [&](std::string* err) { return a->opt.set_step(step, err); });
+}
+
+int ddpb_adamw_get_step(ddpb_adamw_t a, int64_t* step) {
+  if (!a || !step) return fail(DDPB_E_ARG, "adamw get_step: NULL argument");
+  return guarded("adamw get_step", [&](std::string* err) { return a->opt.get_step(step, err); });
 }
 
 }  // extern "C"

@@ -3,9 +3,14 @@
 // defined in core.hpp.
 #include "core.hpp"
 
+#include <atomic>
 #include <utility>
 
 namespace ddpb {
+
+namespace {
+std::atomic<int64_t> g_binds{0};
+}
 
 Reducer::Reducer(Plan plan) : plan_(std::move(plan)), launcher_(make_launcher()) {
   begin_iteration();
@@ -42,6 +47,7 @@ int Reducer::bind(const BindArgs& args, std::string* err) {
     rc = launcher_->bind(plan_, args, err);
   }
   bound_ = (rc == kOk);
+  bind_id_ = ++g_binds;
   static_bind_ = bound_ && args.no_alloc;
   sync_step_set_ = false;          // the launcher's tables were released
   // The launch log and the timing history refer to the previous binding's
@@ -58,6 +64,18 @@ int Reducer::ensure_prior_reduction_finished(std::string* err) {
     failed_ = true;
     *err = "the previous iteration left buckets unreduced; a new iteration cannot start before ddpb_reset";
     return kErrIncomplete;
+  }
+  return kOk;
+}
+
+int Reducer::check_idle(const char* what, std::string* err) const {
+  if (failed_) {
+    *err = std::string(what) + ": the previous iteration left buckets unreduced; call ddpb_reset first";
+    return kErrIncomplete;
+  }
+  if (iteration_open()) {
+    *err = std::string(what) + ": an iteration is in progress; the gradients are final after ddpb_finalize";
+    return kErrState;
   }
   return kOk;
 }

@@ -184,6 +184,13 @@ class Reducer {
   // earlier iterations belong to device resources that no longer exist.
   int64_t timed_from() const { return timed_from_; }
   Launcher* launcher() { return launcher_.get(); }
+  // Names the current binding: another number for every successful bind of the
+  // process, 0 while unbound. What follows the synchronisation (gradient norm,
+  // AdamW) took its gradient addresses from one binding.
+  int64_t bind_id() const { return bound_ ? bind_id_ : 0; }
+  // kErrState while an iteration is open (its buckets may still be reducing),
+  // kErrIncomplete while a failed one is latched.
+  int check_idle(const char* what, std::string* err) const;
 
  private:
   void begin_iteration();
@@ -192,6 +199,7 @@ class Reducer {
   Plan plan_;
   std::unique_ptr<Launcher> launcher_;
   bool bound_ = false;
+  int64_t bind_id_ = 0;
   bool static_bind_ = false;       // bound by ddpb_bind_static: no staging for tables
   bool sync_ = true;
   bool failed_ = false;            // latched "prior reduction did not finish"

@@ -1,10 +1,11 @@
-// null_launcher.cpp -- Launcher that enqueues nothing. Linked only into the
+// null_launcher.cpp -- Launcher and OptimDevice that enqueue nothing. Linked only into the
 // host-only test library so the plan and the readiness state machine can be
 // exercised on a machine without a GPU. It moves no data: gradients are left
 // untouched, so it is never a substitute for the HIP launcher.
 #include <atomic>
 
 #include "core.hpp"
+#include "optim.hpp"
 
 namespace {
 // Joins requested by every null launcher of the process (read by the host
@@ -45,7 +46,27 @@ class NullLauncher final : public Launcher {
   }
 };
 
+class NullOptimDevice final : public OptimDevice {
+ public:
+  int current(int* device, std::string*) override {
+    *device = 0;
+    return kOk;
+  }
+  int upload(int, void*, void*, const void*, size_t, std::string*) override { return kOk; }
+  int download(int, void*, void*, const void*, size_t, std::string* err) override {
+    *err = "no device in the host-only test build";
+    return kErrState;
+  }
+  int norm(const NormLaunch&, std::string*) override { return kOk; }
+  int adamw(const AdamwLaunch&, std::string*) override { return kOk; }
+};
+
 }  // namespace
+
+OptimDevice* optim_device() {
+  static NullOptimDevice d;
+  return &d;
+}
 
 std::unique_ptr<Launcher> make_launcher() { return std::make_unique<NullLauncher>(); }
 

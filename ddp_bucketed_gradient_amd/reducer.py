@@ -13,6 +13,7 @@ from typing import List, Optional, Sequence
 from . import _abi
 from ._abi import (BF16, F32, MODE_FUSED, MODE_STAGED, BIND_DEVICE_TIMESTAMPS, BIND_TIME_LAUNCHES,  # noqa: F401
                    BIND_ROCTX, BIND_OVERLAP)
+from .optim import AdamW, GradNorm
 
 MiB = 1 << 20
 
@@ -43,6 +44,7 @@ class Reducer:
             self._numel.append(n)
         self.h = self.lib.reducer_create(self.shapes, F32, self.cap, self.R)
         self._keep = []
+        self._grads = None           # R x P tensors of the present binding
 
     # -- plan queries -------------------------------------------------------------
     @property
@@ -89,6 +91,7 @@ class Reducer:
         self.compute_stream, self.side_streams, self.workspace = compute, sides, ws
         self.lib.bind(self.h, ptrs, ws.data_ptr() if ws is not None else 0, nbytes, compute.cuda_stream,
                       [s.cuda_stream for s in sides], mode, flags)
+        self._grads = grads
 
     def bind_static(self, grads, compute_stream=None, mode: int = MODE_FUSED):
         """Allocation-free binding (ddpb_bind_static): the library's tables sit
@@ -109,6 +112,7 @@ class Reducer:
         self._keep = [grads, compute]
         self.compute_stream, self.side_streams, self.workspace = compute, [compute], None
         self.lib.bind_static(self.h, ptrs, compute.cuda_stream, mode)
+        self._grads = grads
 
     def bind_bucket_views(self, device=None, compute_stream=None, side_streams=None, flags: int = 0):
         """gradient_as_bucket_view: allocate one flat fp32 storage per replica
@@ -143,6 +147,7 @@ class Reducer:
         self.compute_stream, self.side_streams, self.workspace = compute, sides, None
         self.lib.bind_bucket_views(self.h, [s.data_ptr() for s in stores], n, compute.cuda_stream,
                                    [s.cuda_stream for s in sides], flags)
+        self._grads = views
         return views
 
     def rebuild_buckets(self, bucket_cap_bytes: Optional[int] = None):
@@ -152,6 +157,7 @@ class Reducer:
         cap = self.cap if bucket_cap_bytes is None else int(bucket_cap_bytes)
         self.lib.rebuild_buckets(self.h, cap)
         self.cap = cap
+        self._grads = None
 
     def ready_order(self) -> List[int]:
         return self.lib.get_ready_order(self.h)
@@ -252,6 +258,23 @@ class Reducer:
             raise ValueError(f"used flags must have shape ({self.R}, {self.P})")
         self.lib.set_local_used(self.h, np.ascontiguousarray(u, dtype=np.uint8).ravel())
 
+    # -- after the synchronisation -------------------------------------------------------
+    def _replica_grads(self):
+        if self._grads is None:
+            raise _abi.DdpbError(_abi.E_STATE, "the reducer is not bound to tensors")
+        return self._grads[0]
+
+    def grad_norm(self) -> "GradNorm":
+        """The global norm of the averaged gradients (replica 0's), computed on
+        the compute stream between synchronisations. Made once per binding."""
+        return GradNorm(self._replica_grads(), reducer=self, lib=self.lib)
+
+    def adamw(self, params, **options) -> "AdamW":
+        """AdamW on the averaged gradients: ``params`` R x P (every replica's
+        parameters receive the step) or P tensors; ``options`` as for AdamW.
+        Steps run on the compute stream, behind finalize; made once per binding."""
+        return AdamW(params, self._replica_grads(), reducer=self, lib=self.lib, **options)
+
     # -- diagnostics -------------------------------------------------------------------
     def launch_log(self, with_stamps: bool = False):
         return self.lib.get_launch_log(self.h, with_stamps)
@@ -276,6 +299,7 @@ class Reducer:
             self.lib.destroy(self.h)
             self.h = None
             self._keep = []
+            self._grads = None
             self._keep_steps = None
 
     def __del__(self):

@@ -45,8 +45,8 @@ extern "C" {
 
 typedef struct ddpb_reducer* ddpb_t;
 
-/* element types */
-enum { DDPB_F32 = 0, DDPB_BF16 = 1 };
+/* element types (DDPB_F16: parameters and gradients of the norm and AdamW only) */
+enum { DDPB_F32 = 0, DDPB_BF16 = 1, DDPB_F16 = 2 };
 
 /* kernel modes for ddpb_bind */
 enum {
@@ -370,6 +370,132 @@ int ddpb_set_local_used(ddpb_t h, const uint8_t* used);
  * stream that ran one, so work enqueued on it afterwards cannot race with
  * their copy-back. Errors: DDPB_E_HIP. */
 int ddpb_reset(ddpb_t h);
+
+/* ---------------------------------------------------------------------------
+ * After the synchronisation: the global gradient norm and the AdamW step, over
+ * many tensors in one launch each ([Li] "Gradient Accumulation (no_sync)": the
+ * optimizer step that follows the averaged gradients; [C30] "Finalize Backward
+ * 与梯度可见性": it runs behind finalize on the compute stream).
+ *
+ * Both are handles of their own: create (host only), bind memory and a stream,
+ * then call once per step. All device memory, the workspace included, is the
+ * caller's; the library allocates nothing. Work is enqueued on the bound
+ * stream of the device that was current at the bind (whatever device is
+ * current at the call) and nothing waits for it. Calls may be captured into a
+ * graph and replayed, except bind, set_step and get_step (DDPB_E_STATE): the
+ * count of steps and the clip coefficient live on the device. One handle's
+ * calls must be ordered one after the other, graph replays included.
+ *
+ * The ddpb_t argument (bind, compute, step) may be NULL. With a reducer, bind
+ * notes the reducer's present binding (DDPB_E_STATE if it is unbound), and
+ * compute and step refuse while an iteration is open or the reducer has been
+ * bound again since (DDPB_E_STATE) or a failed iteration is latched
+ * (DDPB_E_INCOMPLETE): the gradients are not the averaged ones then. Pass the
+ * gradient addresses of one replica (they are equal on all) and the reducer's
+ * compute stream.
+ */
+
+/* Global norm of P tensors: norm = grad_scale * sqrt(sum of all squares),
+ * summed in fp64 in a fixed order (the same bits on every run); coef =
+ * max_norm / norm where norm > max_norm, else 1. */
+typedef struct ddpb_norm* ddpb_norm_t;
+
+/* What ddpb_norm_compute leaves in the first 16 bytes of the workspace. */
+struct ddpb_norm_result {
+  float norm;
+  float coef;
+  int32_t skip;       /* 1: the norm was not finite and DDPB_NORM_SKIP_NONFINITE was set */
+  uint32_t reserved;
+};
+
+enum { DDPB_NORM_SKIP_NONFINITE = 1 };
+
+/*   numel    elements of each tensor (>= 0)
+ *   dtypes   DDPB_F32, DDPB_BF16 or DDPB_F16, for each tensor */
+int ddpb_norm_create(const int64_t* numel, const int32_t* dtypes, int32_t P, ddpb_norm_t* out);
+void ddpb_norm_destroy(ddpb_norm_t n);
+int ddpb_norm_workspace_bytes(ddpb_norm_t n, int64_t* bytes);
+
+/*   grads      P device pointers, numel[v] contiguous elements each, aligned to
+ *              their element type (NULL where numel is 0)
+ *   workspace  256-byte aligned, >= ddpb_norm_workspace_bytes; coef starts at 1
+ * Uploads the tables and synchronizes the stream once. */
+int ddpb_norm_bind(ddpb_norm_t n, void* const* grads, void* workspace, int64_t ws_bytes, void* stream, ddpb_t h);
+
+/* max_norm > 0 (may be infinite: coef stays 1); grad_scale finite: the factor
+ * that takes a loss scale out of the gradients. */
+int ddpb_norm_compute(ddpb_norm_t n, ddpb_t h, double max_norm, double grad_scale, int32_t flags);
+
+/* AdamW over P variables. With t the number of the step, per element, in fp32
+ * with one rounding per operation:
+ *   g' = g * (grad_scale * coef)
+ *   m  = beta1 m + (1 - beta1) g'
+ *   v  = beta2 v + (1 - beta2) g' g'            r = sqrt(v)
+ *   p  = p (1 - lr wd) - m / (r / sqrt(1 - beta2^t) + eps) * lr / (1 - beta1^t)
+ * where lr stands for lr * lr_scale[v] and wd for weight_decay[v]. The new p is
+ * written to every replica's parameter; replica 0's is the one that is read
+ * (data-parallel replicas start equal and stay equal).
+ *
+ * State types
+ *   DDPB_STATE_F32  m and v in fp32 (8 bytes per element)
+ *   DDPB_STATE_F8   m and r = sqrt(v) as OCP e4m3 codes, one power-of-two scale
+ *                   (e8m0 byte, 2^(s - 127)) for each block of 64 consecutive
+ *                   elements of a variable: 2 + 2/64 bytes per element. The
+ *                   scale is the smallest with max|x| <= 448 * scale; codes are
+ *                   rounded stochastically (to nearest, v, which moves by 0.1 %
+ *                   a step, would stay on its code), with 16 random bits per
+ *                   value from a hash of (seed, t, index): the same bits on
+ *                   every run. r > 0 never becomes code 0. An element that is
+ *                   not finite becomes NaN. All-zero codes are the zero state. */
+typedef struct ddpb_adamw* ddpb_adamw_t;
+
+enum { DDPB_STATE_F32 = 0, DDPB_STATE_F8 = 1 };
+enum { DDPB_STATE_BLOCK = 64 };
+
+enum { DDPB_ADAMW_MASTER = 1 };   /* 16-bit parameters with an fp32 master copy: the step reads and writes
+                                     the master and rounds it (to nearest even) into the parameters */
+
+/*   numel         elements of each variable (>= 0)
+ *   R             parameter replicas, 1..64
+ *   param_dtype, grad_dtype   DDPB_F32, DDPB_BF16 or DDPB_F16
+ *   state         DDPB_STATE_*;  flags  DDPB_ADAMW_*
+ *   beta1, beta2  in [0, 1);  eps  >= 0, finite
+ *   weight_decay, lr_scale   P values each (>= 0, finite), or NULL for 0 and 1
+ *   seed          of the 8-bit states' random bits */
+int ddpb_adamw_create(const int64_t* numel, int32_t P, int32_t R, int32_t param_dtype, int32_t grad_dtype,
+                      int32_t state, int32_t flags, double beta1, double beta2, double eps,
+                      const double* weight_decay, const double* lr_scale, uint64_t seed, ddpb_adamw_t* out);
+void ddpb_adamw_destroy(ddpb_adamw_t a);
+int ddpb_adamw_workspace_bytes(ddpb_adamw_t a, int64_t* bytes);
+
+/*   params      R * P device pointers, replica-major
+ *   grads       P device pointers
+ *   master      P fp32 pointers (DDPB_ADAMW_MASTER; else NULL)
+ *   exp_avg     P pointers: m, fp32 or codes
+ *   second      P pointers: v in fp32, or codes of r
+ *   avg_scale, root_scale   P pointers to ceil(numel / 64) bytes (DDPB_STATE_F8; else NULL)
+ *   step        steps already done (0 for a new state, which must be all zeros)
+ * Every array contiguous and aligned to its element type (NULL where numel is
+ * 0). The memory that a step writes must not overlap anything else named here:
+ * DDPB_E_ARG for a tied parameter listed twice. Uploads the tables and
+ * synchronizes the stream once. */
+int ddpb_adamw_bind(ddpb_adamw_t a, void* const* params, void* const* grads, void* const* master,
+                    void* const* exp_avg, void* const* second, void* const* avg_scale, void* const* root_scale,
+                    int64_t step, void* workspace, int64_t ws_bytes, void* stream, ddpb_t h);
+
+/*   lr, lr_device  the rate: a host value (finite, >= 0), or, if not NULL, the
+ *                  fp32 at that device address when the step runs (so that a
+ *                  replayed graph follows a schedule)
+ *   clip           NULL, or the workspace of a bound norm whose compute was
+ *                  enqueued before on the same stream: g' takes its coef, and
+ *                  with its skip set the step changes nothing and does not count */
+int ddpb_adamw_step(ddpb_adamw_t a, ddpb_t h, double lr, const float* lr_device, double grad_scale,
+                    const void* clip);
+
+/* The count of steps done: written or read on the bound stream, which is
+ * synchronized. */
+int ddpb_adamw_set_step(ddpb_adamw_t a, int64_t step);
+int ddpb_adamw_get_step(ddpb_adamw_t a, int64_t* step);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics.

@@ -25,10 +25,11 @@ Modules:
   reducer   -- readiness state machine, pack, fixed-order mean, copy-back,
                finalize, no_sync accumulation
   linear10  -- the nn.Linear(10, 10) example in closed form
+  optim     -- gradient norm, AdamW and its 8-bit states, in 64 bits
 
 Pins (all in ``tests/test_oracle_*.py``): the pages' printed layouts, the
 sequence of the in-order launch example, closed forms, exact rational means on
 dyadic inputs, error bounds, brute force over permutations, and planted-mistake
 checks. No function here is "parity unpinned".
 """
-from . import plan, reducer, linear10  # noqa: F401
+from . import plan, reducer, linear10, optim  # noqa: F401

@@ -12,11 +12,6 @@ namespace {
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
-int64_t count_tiles(const std::vector<int64_t>& numel) {
-  int64_t n = 0;
-  for (int64_t k : numel) n += (k + kOptimTile - 1) / kOptimTile;
-  return n;
-}
 
 bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(a) == 0; }
 
@@ -61,7 +56,7 @@ int check_overlap(std::vector<Range>* rs, std::string* err) {
 int ReducerTie::check(const Reducer* red, const char* what, std::string* err) const {
   if (red == nullptr) return kOk;
   if (red->bind_id() != bind_id) {
-    *err = std::string(what) + ": the reducer was bound again after this handle took its gradients; bind this handle again";
+    *err = std::string(what) + ": the reducer was bound again after this handle took its gradients; bind it again";
     return kErrState;
   }
   return red->check_idle(what, err);
@@ -81,12 +76,24 @@ int tie_to(const Reducer* red, const char* what, ReducerTie* tie, std::string* e
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// norm: [result, 256 bytes][partial sums][tiles]
+// norm: [result, 256 bytes][counters][partial sums][tiles]
 
-int64_t Norm::ntiles() const { return count_tiles(numel_); }
+namespace {
+constexpr int64_t kPartialsAt = 256 + (kArriveBytes + 255) / 256 * 256;
+constexpr int64_t kNormTilesAt = kPartialsAt + (kNormBlocks * 8 + 255) / 256 * 256;
+}
+
+int64_t Norm::ntiles() const {
+  int64_t n = 0;
+  for (size_t v = 0; v < numel_.size(); ++v) {
+    const int64_t tile = kNormTileBytes / dtype_size(dtypes_[v]);
+    n += (numel_[v] + tile - 1) / tile;
+  }
+  return n;
+}
 
 int64_t Norm::workspace_bytes() const {
-  return 256 + up256(kNormBlocks * 8) + up256(ntiles() * static_cast<int64_t>(sizeof(NormTile)));
+  return kNormTilesAt + up256(ntiles() * static_cast<int64_t>(sizeof(NormTile)));
 }
 
 int Norm::bind(void* const* grads, void* ws, int64_t ws_bytes, void* stream, const Reducer* red, std::string* err) {
@@ -96,24 +103,26 @@ int Norm::bind(void* const* grads, void* ws, int64_t ws_bytes, void* stream, con
     return kErrArg;
   }
   std::vector<char> h(static_cast<size_t>(workspace_bytes()), 0);
-  NormTile* t = reinterpret_cast<NormTile*>(h.data() + 256 + up256(kNormBlocks * 8));
+  NormTile* t = reinterpret_cast<NormTile*>(h.data() + kNormTilesAt);
   for (size_t v = 0; v < numel_.size(); ++v) {
     if (numel_[v] == 0) continue;
     if (grads[v] == nullptr || !aligned(grads[v], dtype_size(dtypes_[v]))) {
       *err = "norm bind: NULL or misaligned gradient pointer";
       return kErrArg;
     }
-    for (int64_t s = 0; s < numel_[v]; s += kOptimTile)
+    const int64_t tile = kNormTileBytes / dtype_size(dtypes_[v]);
+    for (int64_t s = 0; s < numel_[v]; s += tile)
       *t++ = NormTile{addr(grads[v]) + static_cast<uint64_t>(s * dtype_size(dtypes_[v])),
-                      static_cast<int32_t>(std::min(kOptimTile, numel_[v] - s)), dtypes_[v]};
+                      static_cast<int32_t>(std::min(tile, numel_[v] - s)), dtypes_[v]};
   }
   NormLaunch l{};
   l.stream = stream;
   if (const int rc = optim_device()->current(&l.device, err); rc != kOk) return rc;
   char* base = static_cast<char*>(ws);
   l.result = reinterpret_cast<NormResult*>(base);
-  l.partials = reinterpret_cast<double*>(base + 256);
-  l.tiles = reinterpret_cast<const NormTile*>(base + 256 + up256(kNormBlocks * 8));
+  l.arrived = reinterpret_cast<uint32_t*>(base + 256);
+  l.partials = reinterpret_cast<double*>(base + kPartialsAt);
+  l.tiles = reinterpret_cast<const NormTile*>(base + kNormTilesAt);
   l.ntiles = static_cast<int32_t>(ntiles());
   reinterpret_cast<NormResult*>(h.data())->coef = 1.0f;
   ReducerTie tie;
@@ -144,12 +153,20 @@ int Norm::compute(const Reducer* red, double max_norm, double grad_scale, bool s
 }
 
 // ---------------------------------------------------------------------------
-// AdamW: [scalars, 256 bytes][tiles][replica pointers]
+// AdamW: [scalars, 256 bytes][counters][tiles][replica pointers]
 
-int64_t Adamw::ntiles() const { return count_tiles(c_.numel); }
+namespace {
+constexpr int64_t kTilesAt = 256 + (kArriveBytes + 255) / 256 * 256;
+}
+
+int64_t Adamw::ntiles() const {
+  int64_t n = 0;
+  for (int64_t k : c_.numel) n += (k + kOptimTile - 1) / kOptimTile;
+  return n;
+}
 
 int64_t Adamw::workspace_bytes() const {
-  return 256 + up256(ntiles() * static_cast<int64_t>(sizeof(AdamwTile))) +
+  return kTilesAt + up256(ntiles() * static_cast<int64_t>(sizeof(AdamwTile))) +
          up256(static_cast<int64_t>(c_.R - 1) * static_cast<int64_t>(c_.numel.size()) * 8);
 }
 
@@ -167,8 +184,8 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
   const size_t P = c_.numel.size();
   const int64_t ps = dtype_size(c_.param_dtype), gs = dtype_size(c_.grad_dtype), ss = c_.f8 ? 1 : 4;
   std::vector<char> h(static_cast<size_t>(workspace_bytes()), 0);
-  AdamwTile* t = reinterpret_cast<AdamwTile*>(h.data() + 256);
-  const int64_t rep_at = 256 + up256(ntiles() * static_cast<int64_t>(sizeof(AdamwTile)));
+  AdamwTile* t = reinterpret_cast<AdamwTile*>(h.data() + kTilesAt);
+  const int64_t rep_at = kTilesAt + up256(ntiles() * static_cast<int64_t>(sizeof(AdamwTile)));
   uint64_t* rep = reinterpret_cast<uint64_t*>(h.data() + rep_at);
   std::vector<Range> ranges;
   ranges.reserve(P * static_cast<size_t>(c_.R + 7) + 1);
@@ -233,7 +250,8 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
   l.f8 = c_.f8 ? 1 : 0;
   l.master = c_.master ? 1 : 0;
   l.scalars = reinterpret_cast<StepScalars*>(dev);
-  l.tiles = reinterpret_cast<const AdamwTile*>(dev + 256);
+  l.arrived = reinterpret_cast<uint32_t*>(dev + 256);
+  l.tiles = reinterpret_cast<const AdamwTile*>(dev + kTilesAt);
   l.ntiles = static_cast<int32_t>(ntiles());
   l.replicas = reinterpret_cast<const uint64_t*>(dev + rep_at);
   l.R = c_.R;

@@ -8,8 +8,6 @@
 namespace ddpb {
 namespace {
 
-constexpr int kOptBlock = 256;
-
 #define HIP_OK(expr, what)                                                        \
   do {                                                                            \
     hipError_t e_ = (expr);                                                       \
@@ -47,45 +45,87 @@ template <> struct Elem<kF16> {
   typedef v4h raw;
 };
 
+// A table entry that nothing writes while the kernel runs: a scalar load.
+template <typename T>
+__device__ __forceinline__ T constant(const T* p) {
+  T x;
+  __builtin_memcpy(&x, (const __attribute__((address_space(4))) T*)p, sizeof(T));
+  return x;
+}
+
 template <typename T>
 __device__ __forceinline__ __attribute__((address_space(1))) T* G(uint64_t a) {
   return (__attribute__((address_space(1))) T*)a;
 }
 
-// Elements i .. i+3 of the array at `a`, of which `left` (1..4, or more) exist.
+// Address of element i < 2^30 of the array at `a` (a 32-bit offset, which the
+// memory instructions add for free).
 template <int D>
-__device__ __forceinline__ v4f load4(uint64_t a, int i, int left) {
+__device__ __forceinline__ uint64_t element(uint64_t a, int i) {
+  return a + static_cast<uint32_t>(i) * static_cast<uint32_t>(sizeof(typename Elem<D>::one));
+}
+
+// Elements i .. i+3 of the array at `a`, of which `left` (1..4, or more) exist;
+// FULL: all four do. Every byte is touched once per call, so all accesses are
+// non-temporal.
+template <int D, bool FULL>
+__device__ __forceinline__ typename Elem<D>::raw load4(uint64_t a, int i, int left) {
   typedef typename Elem<D>::one one;
   typedef typename Elem<D>::four four;
-  if (left >= 4) return __builtin_convertvector(*G<const four>(a + static_cast<uint64_t>(i) * sizeof(one)), v4f);
-  v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (FULL || left >= 4) return __builtin_nontemporal_load(G<const four>(element<D>(a, i)));
+  typename Elem<D>::raw x = {};
   const auto* p = G<const one>(a) + i;
-  if (left > 0) x.x = static_cast<float>(p[0]);
-  if (left > 1) x.y = static_cast<float>(p[1]);
-  if (left > 2) x.z = static_cast<float>(p[2]);
+  if (left > 0) x.x = p[0];
+  if (left > 1) x.y = p[1];
+  if (left > 2) x.z = p[2];
   return x;
 }
 
+// Full vectors are stored through a buffer resource over the tile, which lets
+// the store carry device scope beside the non-temporal hint (4 workgroups per
+// CU: 1.62 against 1.65 ms for BERT-large in fp32, 0.245 against 0.264 ms for
+// ResNet-50 with 8 replicas). Only addresses on a multiple of 4.
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+constexpr int kPolicyDeviceNT = 2 | 16;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(uint64_t a) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0,
+                                           kOptimTile * 4, 0x00020000);
+}
+
+template <typename R>
+__device__ __forceinline__ v4f widen(R x) { return __builtin_convertvector(x, v4f); }
+
 // Rounds to nearest even where D has 16 bits: the one rounding a stored
 // parameter goes through (its fp32 master, if there is one, keeps the rest).
-template <int D>
+template <int D, bool FULL>
 __device__ __forceinline__ void store4(uint64_t a, int i, int left, v4f x) {
   typedef typename Elem<D>::one one;
   typedef typename Elem<D>::four four;
   typedef typename Elem<D>::raw raw;
-  if (left >= 4) {
-    *G<four>(a + static_cast<uint64_t>(i) * sizeof(one)) = __builtin_convertvector(x, raw);
+  const raw y = __builtin_convertvector(x, raw);
+  if (FULL && (sizeof(one) == 4 || (a & 3) == 0)) {
+    if constexpr (sizeof(one) == 4)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, y), rsrc(a), i * 4, 0, kPolicyDeviceNT);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, y), rsrc(a), i * 2, 0, kPolicyDeviceNT);
+    return;
+  }
+  if (FULL || left >= 4) {
+    __builtin_nontemporal_store(static_cast<four>(y), G<four>(element<D>(a, i)));
     return;
   }
   auto* p = G<one>(a) + i;
-  if (left > 0) p[0] = static_cast<one>(x.x);
-  if (left > 1) p[1] = static_cast<one>(x.y);
-  if (left > 2) p[2] = static_cast<one>(x.z);
+  if (left > 0) p[0] = y.x;
+  if (left > 1) p[1] = y.y;
+  if (left > 2) p[2] = y.z;
 }
 
+template <bool FULL>
 __device__ __forceinline__ uint32_t load_codes(uint64_t a, int i, int left) {
   typedef uint32_t u1 __attribute__((aligned(1)));
-  if (left >= 4) return *G<const u1>(a + static_cast<uint64_t>(i));
+  if (FULL || left >= 4) return __builtin_nontemporal_load(G<const u1>(a + static_cast<uint32_t>(i)));
   const auto* p = G<const uint8_t>(a) + i;
   uint32_t x = 0;
   if (left > 0) x = p[0];
@@ -94,10 +134,15 @@ __device__ __forceinline__ uint32_t load_codes(uint64_t a, int i, int left) {
   return x;
 }
 
+template <bool FULL>
 __device__ __forceinline__ void store_codes(uint64_t a, int i, int left, uint32_t x) {
   typedef uint32_t u1 __attribute__((aligned(1)));
-  if (left >= 4) {
-    *G<u1>(a + static_cast<uint64_t>(i)) = x;
+  if (FULL && (a & 3) == 0) {
+    __builtin_amdgcn_raw_buffer_store_b32(x, rsrc(a), i, 0, kPolicyDeviceNT);
+    return;
+  }
+  if (FULL || left >= 4) {
+    __builtin_nontemporal_store(x, G<u1>(a + static_cast<uint32_t>(i)));
     return;
   }
   auto* p = G<uint8_t>(a) + i;
@@ -107,10 +152,35 @@ __device__ __forceinline__ void store_codes(uint64_t a, int i, int left, uint32_
 }
 
 // ---------------------------------------------------------------------------
+// Counts a workgroup as done; true for the last one. One counter took 12.4 ns
+// for each workgroup (82,000 tiles: 1.02 ms, whatever else the kernel did), so
+// workgroups count on 64 lines, and the last of each line on one more.
+__device__ __forceinline__ bool last_to_arrive(uint32_t* counters) {
+  const uint32_t slot = blockIdx.x % kArriveSlots;
+  const uint32_t slots = min(gridDim.x, static_cast<uint32_t>(kArriveSlots));
+  const uint32_t mine = (gridDim.x - slot + kArriveSlots - 1) / kArriveSlots;
+  auto count = [&](uint32_t* c, uint32_t all) {
+    if (__hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != all - 1) return false;
+    __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+  };
+  return count(counters + slot * kArriveStride, mine) && count(counters + kArriveSlots * kArriveStride, slots);
+}
+
+// ---------------------------------------------------------------------------
 // Global norm: n = grad_scale * sqrt(sum g^2), coef = max_norm / n if n >
 // max_norm, else 1. Summed in fp64, in an order that only the sizes decide:
 // each lane over its elements, each workgroup over its lanes, the workgroup
 // that finishes last over all partial sums.
+
+//
+// Bound by HBM: 512 workgroups of 512 threads, 16 KiB of a tensor each at a
+// time, two 16-byte loads in flight per lane, non-temporal: 186 us for
+// BERT-large's 1.34 GB in fp32 (7.2 TB/s), 99 us in bf16 (6.8 TB/s). 256 x
+// 1024 threads or 1024 x 256 of them took 191-198 us, one load in flight 284,
+// four 198.
+constexpr int kNormThreads = 512;
+constexpr int kNormUnroll = 2;
 
 __device__ __forceinline__ double block_sum(double x, double* lds) {
 #pragma unroll
@@ -120,41 +190,76 @@ __device__ __forceinline__ double block_sum(double x, double* lds) {
   __syncthreads();
   x = lds[0];
 #pragma unroll
-  for (int w = 1; w < kOptBlock / 64; ++w) x += lds[w];
+  for (int w = 1; w < kNormThreads / 64; ++w) x += lds[w];
   return x;
 }
 
+// 16 bytes of a gradient, or the elements of them that exist, as fp32 pairs.
 template <int D>
-__device__ __forceinline__ double tile_squares(const NormTile& t, double acc) {
-  for (int i = 4 * threadIdx.x; i < t.len; i += 4 * kOptBlock) {
-    const v4f g = load4<D>(t.grad, i, t.len - i);
+struct Chunk {
+  static constexpr int kElems = D == kF32 ? 4 : 8;
+  typedef typename Elem<D>::one raw __attribute__((ext_vector_type(kElems)));
+  typedef raw any __attribute__((aligned(sizeof(typename Elem<D>::one))));
+};
+
+template <int D>
+__device__ __forceinline__ void add_squares(typename Chunk<D>::raw x, double (&acc)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc = __builtin_fma(static_cast<double>(g[j]), static_cast<double>(g[j]), acc);
+  for (int j = 0; j < Chunk<D>::kElems; ++j) {
+    const double y = static_cast<double>(static_cast<float>(x[j]));
+    acc[j & 3] = __builtin_fma(y, y, acc[j & 3]);
   }
-  return acc;
 }
 
-__global__ __launch_bounds__(kOptBlock) void norm_kernel(const NormTile* __restrict__ tiles, int32_t ntiles,
-                                                         double* __restrict__ partials, NormResult* result,
-                                                         double max_norm, double grad_scale, int32_t skip_nonfinite) {
-  __shared__ double lds[kOptBlock / 64];
-  __shared__ bool last;
-  double acc = 0.0;
-  for (int k = blockIdx.x; k < ntiles; k += gridDim.x) {
-    const NormTile t = tiles[k];
-    if (t.dtype == kF32) acc = tile_squares<kF32>(t, acc);
-    else if (t.dtype == kBF16) acc = tile_squares<kBF16>(t, acc);
-    else acc = tile_squares<kF16>(t, acc);
+template <int D>
+__device__ __forceinline__ void tile_squares(const NormTile& t, double (&acc)[4]) {
+  typedef Chunk<D> C;
+  constexpr int kStep = C::kElems * kNormThreads, U = kNormUnroll;
+  const int first = C::kElems * static_cast<int>(threadIdx.x);
+  int at = 0;
+  for (; at + kStep * U <= t.len; at += kStep * U) {
+    typename C::raw x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      x[u] = __builtin_nontemporal_load(G<const typename C::any>(element<D>(t.grad, at + kStep * u + first)));
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) add_squares<D>(x[u], acc);
   }
-  acc = block_sum(acc, lds);
+  for (int i = at + threadIdx.x; i < t.len; i += kNormThreads) {
+    const double y = static_cast<double>(static_cast<float>(G<const typename Elem<D>::one>(t.grad)[i]));
+    acc[0] = __builtin_fma(y, y, acc[0]);
+  }
+}
+
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormTile* __restrict__ tiles, int32_t ntiles,
+                                                            double* partials, uint32_t* arrived, NormResult* result,
+                                                            double max_norm, double grad_scale,
+                                                            int32_t skip_nonfinite) {
+  __shared__ double lds[kNormThreads / 64];
+  __shared__ bool last;
+  double part[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int k = blockIdx.x; k < ntiles; k += gridDim.x) {
+    const NormTile t = constant(tiles + k);
+    if (t.dtype == kF32) tile_squares<kF32>(t, part);
+    else if (t.dtype == kBF16) tile_squares<kBF16>(t, part);
+    else tile_squares<kF16>(t, part);
+  }
+  double acc = block_sum((part[0] + part[1]) + (part[2] + part[3]), lds);
   if (threadIdx.x == 0) {
-    __hip_atomic_store(&partials[blockIdx.x], acc, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(&result->arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    // The exchange has happened where all XCDs see it once its old value is
+    // back: no fence (whose L2 write-back cost 45 ns a workgroup, one after
+    // the other) has to stand between it and the count.
+    const uint64_t old = __hip_atomic_exchange(reinterpret_cast<uint64_t*>(partials + blockIdx.x),
+                                               __builtin_bit_cast(uint64_t, acc), __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" : : "v"(old) : "memory");
+    last = last_to_arrive(arrived);
   }
   __syncthreads();
   if (!last) return;
   acc = 0.0;
-  for (int k = threadIdx.x; k < static_cast<int>(gridDim.x); k += kOptBlock)
+  for (int k = threadIdx.x; k < static_cast<int>(gridDim.x); k += kNormThreads)
     acc += __hip_atomic_load(&partials[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   acc = block_sum(acc, lds);
   if (threadIdx.x == 0) {
@@ -162,18 +267,19 @@ __global__ __launch_bounds__(kOptBlock) void norm_kernel(const NormTile* __restr
     result->norm = static_cast<float>(n);
     result->coef = n > max_norm ? static_cast<float>(max_norm / n) : 1.0f;
     result->skip = skip_nonfinite && !__builtin_isfinite(n);
-    result->arrived = 0;
   }
 }
 
 // ---------------------------------------------------------------------------
 // AdamW.
 
-// The 16 + 16 random bits of elements 4 group .. 4 group + 3 (high half: m,
-// low half: r), counter-based: multiply and xor-shift rounds over the group's
-// index under the step's key, then a short round per element.
-__device__ __forceinline__ v4u random_bits(uint64_t group, uint32_t key0, uint32_t key1) {
-  uint32_t h = static_cast<uint32_t>(group) * 0x9C8E5A6Du + static_cast<uint32_t>(group >> 32) * 0x7F4A3C15u + key0;
+// The 16 + 16 random bits of four elements (high half: m, low half: r),
+// counter-based: multiply and xor-shift rounds over the group's index under the
+// step's key, then a short round per element. `h` is the first product plus
+// the first key word, which the caller carries along.
+constexpr uint32_t kHashIndex = 0x9C8E5A6Du, kHashHigh = 0x7F4A3C15u;
+
+__device__ __forceinline__ v4u random_bits(uint32_t h, uint32_t key1) {
   h ^= h >> 15;
   h *= 0x85D3B2A7u;
   h ^= (h >> 13) ^ key1;
@@ -206,52 +312,78 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x) {
 __device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
 __device__ __forceinline__ uint32_t as_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 
+// Values of four codes under a scale, 2^(scale - 127).
 __device__ __forceinline__ v4f decode4(uint32_t codes, uint32_t scale) {
-  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(codes), false);
-  const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(codes), true);
   const float f = as_float(scale << 23);
-  return v4f{lo[0] * f, lo[1] * f, hi[0] * f, hi[1] * f};
+  const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes, f, false);
+  const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes, f, true);
+  return v4f{lo[0], lo[1], hi[0], hi[1]};
 }
 
-// e4m3 codes of four elements and the scale of their block (the 64 elements of
-// the lane's row). The scale is the smallest power of two with max|x| / scale
-// <= 448; then |x| / scale is cut to 3 fraction bits after the random bits are
-// added below them (below 2^-6, where all steps are 2^-9, 2^-6 is added first
-// so that the same cut falls on 2^-9). ROOT: r > 0 keeps at least the smallest
-// code, since the step divides by it. Elements that are not finite become NaN
-// and do not count for the scale.
-template <bool ROOT>
-__device__ __forceinline__ uint32_t encode4(v4f x, v4u random, uint32_t* scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t a = as_bits(x[j]) & 0x7FFFFFFFu;
-    top = max(top, a < 0x7F800000u ? a : 0u);
+// e4m3 codes of four elements and the scale of their block, the 64 elements of
+// the lane's row, whose largest magnitude has the bits `top`. The scale is the
+// smallest power of two with max|x| / scale <= 448; the hardware's stochastic
+// conversion divides by it, adds the random bits below the 3 fraction bits (or
+// below the step of 2^-9 under 2^-6) and cuts there. ROOT: r > 0 keeps at
+// least the smallest code, since the step divides by it. x is 2^SHIFT times
+// the value that is stored.
+template <bool ROOT, int SHIFT>
+__device__ __forceinline__ uint32_t encode4(v4f x, uint32_t top, v4u random, uint32_t* scale) {
+  const int s = max(static_cast<int>((top + 0x1FFFFFu) >> 23) - 8, 1 + SHIFT);
+  *scale = static_cast<uint32_t>(s - SHIFT);
+  const float f = as_float(static_cast<uint32_t>(s) << 23);
+  int codes = 0;
+#define DDPB_SR(J)                                                                                     \
+  {                                                                                                    \
+    const float y = ROOT ? __builtin_fmaxf(x[J], x[J] > 0.0f ? f * 0.001953125f : 0.0f) : x[J];       \
+    const uint32_t u = ROOT ? random[J] << 16 : random[J] & 0xFFFF0000u;                               \
+    codes = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(codes, y, u, f, J);                               \
   }
-  top = row_max(top);
-  const int s = max(static_cast<int>(top >> 23) + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0) - 8, 1);
-  *scale = static_cast<uint32_t>(s);
-  const float inv = as_float(static_cast<uint32_t>(254 - s) << 23);
-  float z[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t u = ROOT ? (random[j] & 0xFFFFu) << 4 : (random[j] >> 16) << 4;
-    const float y = __builtin_fabsf(x[j]) * inv;
-    const float low = y < 0.015625f ? 0.015625f : 0.0f;
-    float c = as_float((as_bits(y + low) + u) & 0xFFF00000u) - low;
-    if (ROOT && y > 0.0f) c = __builtin_fmaxf(c, 0.001953125f);
-    c = __builtin_copysignf(c, x[j]);
-    z[j] = __builtin_isfinite(x[j]) ? c : __builtin_nanf("");
-  }
-  int codes = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
-  codes = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], codes, true);
+  DDPB_SR(0) DDPB_SR(1) DDPB_SR(2) DDPB_SR(3)
+#undef DDPB_SR
   return static_cast<uint32_t>(codes);
+}
+
+constexpr uint32_t kInf = 0x7F800000u;
+__device__ __forceinline__ uint32_t magnitude(float x) { return as_bits(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t top4(v4f x) {
+  return max(max(magnitude(x.x), magnitude(x.y)), max(magnitude(x.z), magnitude(x.w)));
+}
+
+// The same for values of any kind: those that are not finite become NaN and do
+// not count for the scale.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode4_any(v4f x, v4u random, uint32_t* scale) {
+  uint32_t nan = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (magnitude(x[j]) >= kInf) {
+      x[j] = 0.0f;
+      nan |= 0x7Fu << (8 * j);
+    }
+  return encode4<ROOT, 0>(x, row_max(top4(x)), random, scale) | nan;
+}
+
+// Square root and quotient, correctly rounded for normal arguments whose
+// results are normal (no difference from the IEEE sequences in 16.8 M random
+// arguments each) in 9 and 7 issue slots instead of 16 and 15: an estimate, its
+// residual by fma, one correction. The 8-bit step is bound by instructions.
+__device__ __forceinline__ float fast_sqrt(float v) {
+  const float h = __builtin_fminf(__builtin_amdgcn_rsqf(v), 0x1p64f);   // v = 0: r = 0
+  const float r = v * h;
+  return __builtin_fmaf(__builtin_fmaf(-r, r, v), 0.5f * h, r);
+}
+__device__ __forceinline__ float fast_div(float x, float d) {
+  const float c = __builtin_amdgcn_rcpf(d);
+  const float q = x * c;
+  return __builtin_fmaf(__builtin_fmaf(-d, q, x), c, q);
 }
 
 struct AdamwArgs {
   const AdamwTile* tiles;
   const uint64_t* replicas;
   StepScalars* scalars;
+  uint32_t* arrived;
   const NormResult* clip;
   const float* lr_device;
   double lr, beta1d, beta2d;
@@ -260,77 +392,184 @@ struct AdamwArgs {
   int32_t ntiles, R, P;
 };
 
+// What a lane reads for four elements, as stored.
+template <int SD, int GD, bool F8>
+struct Quad {
+  typename Elem<SD>::raw w;
+  typename Elem<GD>::raw g;
+  v4f m, v;                    // fp32 states
+  uint32_t mc, rc, ms, rs;     // codes and scales
+};
+
+template <int SD, int GD, bool F8, bool FULL>
+__device__ __forceinline__ void load_quad(Quad<SD, GD, F8>& q, const AdamwTile& t, int i) {
+  const int left = t.len - i;
+  q.w = load4<SD, FULL>(t.src, i, left);
+  q.g = load4<GD, FULL>(t.grad, i, left);
+  if constexpr (F8) {
+    q.mc = load_codes<FULL>(t.avg, i, left);
+    q.rc = load_codes<FULL>(t.second, i, left);
+    q.ms = q.rs = 0;
+    if (FULL || left > 0) {
+      q.ms = G<const uint8_t>(t.avg_scale)[static_cast<uint32_t>(i) / static_cast<uint32_t>(kStateBlock)];
+      q.rs = G<const uint8_t>(t.root_scale)[static_cast<uint32_t>(i) / static_cast<uint32_t>(kStateBlock)];
+    }
+  } else {
+    q.m = load4<kF32, FULL>(t.avg, i, left);
+    q.v = load4<kF32, FULL>(t.second, i, left);
+  }
+}
+
+struct StepValues {      // of the step, in registers
+  float gs, inv_rbc2;
+  uint32_t key0, key1;
+  float decay, rate;     // of the tile's variable
+  uint32_t hash;         // random_bits' h of the lane's first group in the tile
+};
+
+template <int PD, bool MASTER, bool FULL>
+__device__ __forceinline__ void store_params(v4f w, const AdamwTile& t, int i, const AdamwArgs& a) {
+  const int left = t.len - i;
+  store4<PD, FULL>(t.out, i, left, w);
+  if constexpr (MASTER) store4<kF32, FULL>(t.src, i, left, w);
+  for (int rep = 1; rep < a.R; ++rep)
+    store4<PD, FULL>(a.replicas[static_cast<int64_t>(rep - 1) * a.P + t.var] +
+                         static_cast<uint64_t>(t.start) * sizeof(typename Elem<PD>::one),
+                     i, left, w);
+}
+
+template <int PD, int GD, bool MASTER, bool FULL>
+__device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, false>& q, const AdamwTile& t, int at,
+                                            int lane4, const AdamwArgs& a, const StepValues& s) {
+  const int i = at + lane4, left = t.len - i;
+  const v4f g = widen(q.g) * s.gs;
+  const v4f m = q.m * a.beta1 + g * a.one_minus_beta1;
+  const v4f v = q.v * a.beta2 + (g * g) * a.one_minus_beta2;
+  v4f w = widen(q.w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = w[j] * s.decay - (m[j] / (__builtin_sqrtf(v[j]) * s.inv_rbc2 + a.eps)) * s.rate;
+  store_params<PD, MASTER, FULL>(w, t, i, a);
+  store4<kF32, FULL>(t.avg, i, left, m);
+  store4<kF32, FULL>(t.second, i, left, v);
+}
+
+// 8-bit states. v and r are carried as 2^64 v and 2^32 r, so that no v > 0 is
+// below the normal range that fast_sqrt needs; what then overflows (r > 4e9),
+// or is not finite, takes the way without shortcuts, its whole wave with it.
+template <int PD, int GD, bool MASTER, bool FULL>
+__device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, true>& q, const AdamwTile& t, int at,
+                                            int lane4, const AdamwArgs& a, const StepValues& s) {
+  const int i = at + lane4, left = t.len - i;
+  const v4f g = widen(q.g) * s.gs;
+  const v4f m = decode4(q.mc, q.ms) * a.beta1 + g * a.one_minus_beta1;
+  v4f v = decode4(q.rc, min(q.rs, 222u) + 32u);
+  v = (v * v) * a.beta2 + (g * g) * (a.one_minus_beta2 * 0x1p64f);
+  v4f w = widen(q.w), r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r[j] = fast_sqrt(v[j]);
+    w[j] = w[j] * s.decay - fast_div(m[j], r[j] * (s.inv_rbc2 * 0x1p-32f) + a.eps) * s.rate;
+  }
+  const uint32_t mtop = top4(m), rtop = max(max(as_bits(r.x), as_bits(r.y)), max(as_bits(r.z), as_bits(r.w)));
+  const v4u random = random_bits(s.hash + static_cast<uint32_t>(at / 4) * kHashIndex, s.key1);
+  uint32_t ms, rs, mc, rc;
+  if (__builtin_expect(__any(max(mtop, rtop) >= kInf), 0)) {
+    v = decode4(q.rc, q.rs);
+    v = (v * v) * a.beta2 + (g * g) * a.one_minus_beta2;
+    w = widen(q.w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r[j] = __builtin_sqrtf(v[j]);
+      w[j] = w[j] * s.decay - (m[j] / (r[j] * s.inv_rbc2 + a.eps)) * s.rate;
+    }
+    mc = encode4_any<false>(m, random, &ms);
+    rc = encode4_any<true>(r, random, &rs);
+  } else {
+    mc = encode4<false, 0>(m, row_max(mtop), random, &ms);
+    rc = encode4<true, 32>(r, row_max(rtop), random, &rs);
+  }
+  store_params<PD, MASTER, FULL>(w, t, i, a);
+  store_codes<FULL>(t.avg, i, left, mc);
+  store_codes<FULL>(t.second, i, left, rc);
+  if ((threadIdx.x & 15) == 0 && (FULL || left > 0)) {
+    G<uint8_t>(t.avg_scale)[static_cast<uint32_t>(i) / static_cast<uint32_t>(kStateBlock)] = static_cast<uint8_t>(ms);
+    G<uint8_t>(t.root_scale)[static_cast<uint32_t>(i) / static_cast<uint32_t>(kStateBlock)] = static_cast<uint8_t>(rs);
+  }
+}
+
+// How a step is cut into workgroups; none of them loops.
+//
+// 32-bit states are bound by HBM (28 bytes and some 45 instructions an
+// element). One wave and 256 elements per workgroup, 16
+// workgroups per CU (each reserves 1/16 of the LDS, which the kernel does not
+// use): the accesses of the whole GPU then move through every array in step.
+// BERT-large, fp32: 1.454 ms (6.45 TB/s) against 1.55 with workgroups of 256
+// threads at the same waves per CU, 1.52 without the limit, 1.57 at 8 per CU,
+// 1.61 with two groups per lane; with workgroups of 256 threads that loop over
+// 4096 elements, 1.68; with plain loads and stores, 1.79.
+//
+// 8-bit states are bound by instructions as much as by HBM (16 bytes and some
+// 60 issue slots an element in fp32, 10 in bf16): full occupancy, workgroups
+// of 256 threads, since each costs a start. Where the parameters are 16-bit
+// and have no master, two groups per lane: BERT-large 0.563 ms against 0.592
+// with one; with fp32 parameters one: 0.858 ms against 0.905.
+template <int PD, bool MASTER, bool F8>
+struct Shape {
+  static constexpr int kThreads = F8 ? 256 : 64;
+  static constexpr int kU = F8 && PD != kF32 && !MASTER ? 2 : 1;
+  static constexpr int kPart = 4 * kThreads * kU;          // elements per workgroup
+  static constexpr int kParts = kOptimTile / kPart;
+  static constexpr int kLds = F8 ? 0 : 160 * 1024 / 16;
+  static_assert(kParts * kPart == kOptimTile, "a tile is a whole number of parts");
+};
+
 template <int PD, int GD, bool MASTER, bool F8>
-__global__ __launch_bounds__(kOptBlock) void adamw_kernel(const AdamwArgs a) {
+__global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads)) void adamw_kernel(const AdamwArgs a) {
   constexpr int SD = MASTER ? kF32 : PD;
-  float gs = a.grad_scale;
+  typedef Shape<PD, MASTER, F8> S;
+  constexpr int U = S::kU, kStep = 4 * S::kThreads;
+  StepValues s;
+  s.gs = a.grad_scale;
   if (a.clip != nullptr) {
     if (a.clip->skip) return;            // every workgroup alike: the step does not count
-    gs *= a.clip->coef;
+    s.gs *= a.clip->coef;
   }
-  const StepScalars sc = *a.scalars;
+  const StepScalars sc = constant(a.scalars);
+  s.inv_rbc2 = sc.inv_rbc2;
+  s.key0 = sc.key0;
+  s.key1 = sc.key1;
   const double lr = a.lr_device != nullptr ? static_cast<double>(*a.lr_device) : a.lr;
-  for (int k = blockIdx.x; k < a.ntiles; k += gridDim.x) {
-    const AdamwTile t = a.tiles[k];
-    const float decay = static_cast<float>(1.0 - lr * t.lr_scale * t.weight_decay);
-    const float rate = static_cast<float>(lr * t.lr_scale * sc.inv_bc1);
-    // all lanes of a wave stay in the loop together (row_max), those beyond
-    // the end on zeros that are not stored
-    for (int i0 = 0; i0 < t.len; i0 += 4 * kOptBlock) {
-      const int i = i0 + 4 * static_cast<int>(threadIdx.x);
-      const int left = t.len - i;
-      v4f w = load4<SD>(t.src, i, left);
-      const v4f g = load4<GD>(t.grad, i, left) * gs;
-      v4f m, v;
-      if constexpr (F8) {
-        uint32_t ms = 0, rs = 0;
-        if (left > 0) {
-          ms = G<const uint8_t>(t.avg_scale)[i / kStateBlock];
-          rs = G<const uint8_t>(t.root_scale)[i / kStateBlock];
-        }
-        m = decode4(load_codes(t.avg, i, left), ms);
-        v = decode4(load_codes(t.second, i, left), rs);
-        v = v * v;
-      } else {
-        m = load4<kF32>(t.avg, i, left);
-        v = load4<kF32>(t.second, i, left);
-      }
-      m = m * a.beta1 + g * a.one_minus_beta1;
-      v = v * a.beta2 + (g * g) * a.one_minus_beta2;
-      v4f r;
+  const int k = blockIdx.x / S::kParts, at = blockIdx.x % S::kParts * S::kPart;
+  if (k < a.ntiles) {
+    const AdamwTile t = constant(a.tiles + k);
+    s.decay = static_cast<float>(1.0 - lr * t.lr_scale * t.weight_decay);
+    s.rate = static_cast<float>(lr * t.lr_scale * sc.inv_bc1);
+    // Tiles start on multiples of 64, so none crosses a multiple of 2^32 groups.
+    s.hash = (static_cast<uint32_t>(t.group0) + threadIdx.x) * kHashIndex +
+             static_cast<uint32_t>(t.group0 >> 32) * kHashHigh + s.key0;
+    const int i = 4 * static_cast<int>(threadIdx.x);
+    if (at + S::kPart <= t.len) {
+      Quad<SD, GD, F8> q[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r[j] = __builtin_sqrtf(v[j]);
-        w[j] = w[j] * decay - (m[j] / (r[j] * sc.inv_rbc2 + a.eps)) * rate;
-      }
-      store4<PD>(t.out, i, left, w);
-      if constexpr (MASTER) store4<kF32>(t.src, i, left, w);
-      for (int rep = 1; rep < a.R; ++rep)
-        store4<PD>(a.replicas[static_cast<int64_t>(rep - 1) * a.P + t.var] +
-                       static_cast<uint64_t>(t.start) * sizeof(typename Elem<PD>::one),
-                   i, left, w);
-      if constexpr (F8) {
-        const v4u random = random_bits(t.group0 + static_cast<uint64_t>(i >> 2), sc.key0, sc.key1);
-        uint32_t ms, rs;
-        const uint32_t mc = encode4<false>(m, random, &ms);
-        const uint32_t rc = encode4<true>(r, random, &rs);
-        store_codes(t.avg, i, left, mc);
-        store_codes(t.second, i, left, rc);
-        if ((threadIdx.x & 15) == 0 && left > 0) {
-          G<uint8_t>(t.avg_scale)[i / kStateBlock] = static_cast<uint8_t>(ms);
-          G<uint8_t>(t.root_scale)[i / kStateBlock] = static_cast<uint8_t>(rs);
-        }
-      } else {
-        store4<kF32>(t.avg, i, left, m);
-        store4<kF32>(t.second, i, left, v);
+      for (int u = 0; u < U; ++u) load_quad<SD, GD, F8, true>(q[u], t, at + kStep * u + i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) update_quad<PD, GD, MASTER, true>(q[u], t, at + kStep * u, i, a, s);
+    } else {
+      // All lanes of a wave stay in the loop together (row_max), those beyond
+      // the end on zeros that are not stored.
+      for (int e = at; e < min(t.len, at + S::kPart); e += kStep) {
+        Quad<SD, GD, F8> q;
+        load_quad<SD, GD, F8, false>(q, t, e + i);
+        update_quad<PD, GD, MASTER, false>(q, t, e, i, a, s);
       }
     }
   }
   // The workgroup that is done last has seen every other read the scalars: it
   // advances them for the next step.
   __syncthreads();
-  if (threadIdx.x == 0 &&
-      __hip_atomic_fetch_add(&a.scalars->arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1)
+  if (threadIdx.x == 0 && last_to_arrive(a.arrived))
     *a.scalars = step_scalars(sc.done + 1, a.beta1d, a.beta2d, a.seed);
 }
 
@@ -358,8 +597,9 @@ class OnDevice {
 
 template <int PD, int GD, bool MASTER, bool F8>
 void launch_adamw(const AdamwArgs& a, hipStream_t s) {
-  const int blocks = a.ntiles > 0 ? a.ntiles : 1;
-  hipLaunchKernelGGL((adamw_kernel<PD, GD, MASTER, F8>), dim3(blocks), dim3(kOptBlock), 0, s, a);
+  typedef Shape<PD, MASTER, F8> S;
+  const unsigned blocks = static_cast<unsigned>(a.ntiles > 0 ? a.ntiles : 1) * S::kParts;
+  hipLaunchKernelGGL((adamw_kernel<PD, GD, MASTER, F8>), dim3(blocks), dim3(S::kThreads), S::kLds, s, a);
 }
 
 template <int PD, int GD>
@@ -396,8 +636,8 @@ class HipOptimDevice final : public OptimDevice {
     const OnDevice on(l.device);
     if (!on.ok()) return no_device(err);
     const int blocks = l.ntiles < kNormBlocks ? (l.ntiles > 0 ? l.ntiles : 1) : kNormBlocks;
-    hipLaunchKernelGGL(norm_kernel, dim3(blocks), dim3(kOptBlock), 0, static_cast<hipStream_t>(l.stream), l.tiles,
-                       l.ntiles, l.partials, l.result, l.max_norm, l.grad_scale, l.skip_nonfinite);
+    hipLaunchKernelGGL(norm_kernel, dim3(blocks), dim3(kNormThreads), 0, static_cast<hipStream_t>(l.stream), l.tiles,
+                       l.ntiles, l.partials, l.arrived, l.result, l.max_norm, l.grad_scale, l.skip_nonfinite);
     HIP_OK(hipGetLastError(), "launch norm_kernel");
     return kOk;
   }
@@ -409,6 +649,7 @@ class HipOptimDevice final : public OptimDevice {
     a.tiles = l.tiles;
     a.replicas = l.replicas;
     a.scalars = l.scalars;
+    a.arrived = l.arrived;
     a.clip = l.clip;
     a.lr_device = l.lr_device;
     a.lr = l.lr;

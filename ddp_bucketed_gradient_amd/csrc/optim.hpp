@@ -22,13 +22,21 @@ namespace ddpb {
 enum DType : int32_t { kF32 = 0, kBF16 = 1, kF16 = 2 };
 constexpr int64_t dtype_size(int32_t d) { return d == kF32 ? 4 : 2; }
 
-// Elements per 8-bit block (one shared scale), and per tile: one workgroup
-// processes a tile at a time. Tiles start on block boundaries.
+// Elements that share the scale of an 8-bit state.
 constexpr int64_t kStateBlock = 64;
+// Elements per tile, the entry of AdamW's table (96 bytes, so 0.02 an element);
+// tiles start on block boundaries and several workgroups share one.
 constexpr int64_t kOptimTile = 4096;
-// Workgroups of the norm kernel, each of which leaves one partial sum. Fixed,
-// so that the order of the sum does not depend on the device.
-constexpr int32_t kNormBlocks = 1024;
+// The norm's tiles, and its workgroups, each of which leaves one partial sum:
+// constants, so that the order of the sum does not depend on the device.
+constexpr int64_t kNormTileBytes = 16384;
+constexpr int32_t kNormBlocks = 512;
+
+// Counters of the workgroups that are done, kArriveSlots of them and one of
+// the slots, each in a cache line of its own. All return to 0 with the last.
+constexpr int kArriveSlots = 64;
+constexpr int kArriveStride = 32;   // uint32 per counter
+constexpr int64_t kArriveBytes = (kArriveSlots + 1) * kArriveStride * 4;
 
 // Device-side work descriptors, read by the kernels.
 struct NormTile {
@@ -55,12 +63,12 @@ struct AdamwTile {
 };
 static_assert(sizeof(AdamwTile) == 96, "tile layout is shared with the kernels");
 
-// What a norm leaves on the device (ddpb_norm_result, then the library's own).
+// What a norm leaves on the device (ddpb_norm_result).
 struct NormResult {
   float norm;
   float coef;
   int32_t skip;
-  uint32_t arrived;   // workgroups done; back to 0 when the last one is
+  uint32_t pad;
 };
 static_assert(sizeof(NormResult) == 16, "layout is shared with the header");
 
@@ -71,7 +79,7 @@ struct StepScalars {
   double inv_bc1;     // 1 / (1 - beta1^t), t = done + 1
   float inv_rbc2;     // 1 / sqrt(1 - beta2^t)
   uint32_t key0, key1;
-  uint32_t arrived;
+  uint32_t pad;
 };
 static_assert(sizeof(StepScalars) == 32, "layout is shared with the kernels");
 
@@ -98,7 +106,7 @@ DDPB_HD inline StepScalars step_scalars(int64_t done, double beta1, double beta2
   k ^= k >> 32;
   s.key0 = static_cast<uint32_t>(k);
   s.key1 = static_cast<uint32_t>(k >> 32);
-  s.arrived = 0;
+  s.pad = 0;
   return s;
 }
 
@@ -108,6 +116,7 @@ struct NormLaunch {
   const NormTile* tiles;
   int32_t ntiles;
   double* partials;
+  uint32_t* arrived;          // kArriveBytes
   NormResult* result;
   double max_norm, grad_scale;
   int32_t skip_nonfinite;
@@ -122,6 +131,7 @@ struct AdamwLaunch {
   const uint64_t* replicas;   // (R - 1) * P parameter addresses, replica-major
   int32_t R, P;
   StepScalars* scalars;
+  uint32_t* arrived;          // kArriveBytes
   const NormResult* clip;     // or NULL
   const float* lr_device;     // or NULL: lr
   double lr, grad_scale;
@@ -154,7 +164,8 @@ struct ReducerTie {
 
 class Norm {
  public:
-  Norm(std::vector<int64_t> numel, std::vector<int32_t> dtypes) : numel_(std::move(numel)), dtypes_(std::move(dtypes)) {}
+  Norm(std::vector<int64_t> numel, std::vector<int32_t> dtypes)
+      : numel_(std::move(numel)), dtypes_(std::move(dtypes)) {}
   int64_t workspace_bytes() const;
   int bind(void* const* grads, void* ws, int64_t ws_bytes, void* stream, const Reducer* red, std::string* err);
   int compute(const Reducer* red, double max_norm, double grad_scale, bool skip_nonfinite, std::string* err);

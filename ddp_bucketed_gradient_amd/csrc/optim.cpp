@@ -194,7 +194,7 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
   for (size_t v = 0; v < P; ++v) {
     const int64_t n = c_.numel[v];
     if (n == 0) continue;
-    const int64_t blocks = (n + kStateBlock - 1) / kStateBlock;
+    const int64_t blocks = (n + int64_t(kStateBlock) - 1) / int64_t(kStateBlock);
     bool ok = true;
     auto take = [&](const void* p, int64_t size, int64_t bytes, bool written) {
       ok = ok && p != nullptr && aligned(p, size);
@@ -225,8 +225,8 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
       x.avg = addr(b.avg[v]) + static_cast<uint64_t>(s * ss);
       x.second = addr(b.second[v]) + static_cast<uint64_t>(s * ss);
       if (c_.f8) {
-        x.avg_scale = addr(b.avg_scale[v]) + static_cast<uint64_t>(s / kStateBlock);
-        x.root_scale = addr(b.root_scale[v]) + static_cast<uint64_t>(s / kStateBlock);
+        x.avg_scale = addr(b.avg_scale[v]) + static_cast<uint64_t>(s) / kStateBlock;
+        x.root_scale = addr(b.root_scale[v]) + static_cast<uint64_t>(s) / kStateBlock;
       }
       x.len = static_cast<int32_t>(std::min(kOptimTile, n - s));
       x.var = static_cast<int32_t>(v);

@@ -312,6 +312,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x) {
 __device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
 __device__ __forceinline__ uint32_t as_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 
+constexpr uint32_t kInf = 0x7F800000u;
+
 // Values of four codes under a scale, 2^(scale - 127).
 __device__ __forceinline__ v4f decode4(uint32_t codes, uint32_t scale) {
   const float f = as_float(scale << 23);
@@ -329,13 +331,17 @@ __device__ __forceinline__ v4f decode4(uint32_t codes, uint32_t scale) {
 // the value that is stored.
 template <bool ROOT, int SHIFT>
 __device__ __forceinline__ uint32_t encode4(v4f x, uint32_t top, v4u random, uint32_t* scale) {
-  const int s = max(static_cast<int>((top + 0x1FFFFFu) >> 23) - 8, 1 + SHIFT);
-  *scale = static_cast<uint32_t>(s - SHIFT);
-  const float f = as_float(static_cast<uint32_t>(s) << 23);
+  // top's exponent, one more if its fraction is over 3/4, less 8; as the bits of a float
+  const uint32_t bits = max(top + 0x1FFFFFu, static_cast<uint32_t>(9 + SHIFT) << 23) - (8u << 23);
+  *scale = (bits >> 23) - SHIFT;
+  const float f = as_float(bits & kInf);
+  const float least = f * 0x1p-9f;       // r = 0: 0 is the middle one; else r 2^127 is over `least` (r < 2^64, > 2^-43)
   int codes = 0;
 #define DDPB_SR(J)                                                                                     \
   {                                                                                                    \
-    const float y = ROOT ? __builtin_fmaxf(x[J], x[J] > 0.0f ? f * 0.001953125f : 0.0f) : x[J];       \
+    const float y = !ROOT ? x[J]                                                                       \
+                    : SHIFT ? __builtin_amdgcn_fmed3f(x[J], least, x[J] * 0x1p127f)                    \
+                            : __builtin_fmaxf(x[J], x[J] > 0.0f ? least : 0.0f);                       \
     const uint32_t u = ROOT ? random[J] << 16 : random[J] & 0xFFFF0000u;                               \
     codes = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(codes, y, u, f, J);                               \
   }
@@ -344,7 +350,6 @@ __device__ __forceinline__ uint32_t encode4(v4f x, uint32_t top, v4u random, uin
   return static_cast<uint32_t>(codes);
 }
 
-constexpr uint32_t kInf = 0x7F800000u;
 __device__ __forceinline__ uint32_t magnitude(float x) { return as_bits(x) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t top4(v4f x) {
   return max(max(magnitude(x.x), magnitude(x.y)), max(magnitude(x.z), magnitude(x.w)));
@@ -411,8 +416,9 @@ __device__ __forceinline__ void load_quad(Quad<SD, GD, F8>& q, const AdamwTile& 
     q.rc = load_codes<FULL>(t.second, i, left);
     q.ms = q.rs = 0;
     if (FULL || left > 0) {
-      q.ms = G<const uint8_t>(t.avg_scale)[static_cast<uint32_t>(i) / static_cast<uint32_t>(kStateBlock)];
-      q.rs = G<const uint8_t>(t.root_scale)[static_cast<uint32_t>(i) / static_cast<uint32_t>(kStateBlock)];
+      const uint32_t block = static_cast<uint32_t>(i) / kStateBlock;
+      q.ms = G<const uint8_t>(t.avg_scale)[block];
+      q.rs = G<const uint8_t>(t.root_scale)[block];
     }
   } else {
     q.m = load4<kF32, FULL>(t.avg, i, left);
@@ -422,6 +428,7 @@ __device__ __forceinline__ void load_quad(Quad<SD, GD, F8>& q, const AdamwTile& 
 
 struct StepValues {      // of the step, in registers
   float gs, inv_rbc2;
+  float gm, gv;          // factors of g in m and of g^2 in 2^64 v
   uint32_t key0, key1;
   float decay, rate;     // of the tile's variable
   uint32_t hash;         // random_bits' h of the lane's first group in the tile
@@ -454,29 +461,35 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, f
   store4<kF32, FULL>(t.second, i, left, v);
 }
 
-// 8-bit states. v and r are carried as 2^64 v and 2^32 r, so that no v > 0 is
+// 8-bit states, with products that feed a sum fused into it (fewer roundings
+// and instructions than one by one). v and r are carried as 2^64 v and 2^32 r, so that no v > 0 is
 // below the normal range that fast_sqrt needs; what then overflows (r > 4e9),
 // or is not finite, takes the way without shortcuts, its whole wave with it.
 template <int PD, int GD, bool MASTER, bool FULL>
 __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, true>& q, const AdamwTile& t, int at,
                                             int lane4, const AdamwArgs& a, const StepValues& s) {
   const int i = at + lane4, left = t.len - i;
-  const v4f g = widen(q.g) * s.gs;
-  const v4f m = decode4(q.mc, q.ms) * a.beta1 + g * a.one_minus_beta1;
-  v4f v = decode4(q.rc, min(q.rs, 222u) + 32u);
-  v = (v * v) * a.beta2 + (g * g) * (a.one_minus_beta2 * 0x1p64f);
-  v4f w = widen(q.w), r;
+  const v4f g = widen(q.g);
+  v4f m = decode4(q.mc, q.ms), v = decode4(q.rc, min(q.rs, 222u) + 32u), w = widen(q.w), r;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    m[j] = __builtin_fmaf(g[j], s.gm, m[j] * a.beta1);
+    v[j] = __builtin_fmaf(g[j] * g[j], s.gv, v[j] * v[j] * a.beta2);
     r[j] = fast_sqrt(v[j]);
-    w[j] = w[j] * s.decay - fast_div(m[j], r[j] * (s.inv_rbc2 * 0x1p-32f) + a.eps) * s.rate;
+    w[j] = __builtin_fmaf(-fast_div(m[j], __builtin_fmaf(r[j], s.inv_rbc2 * 0x1p-32f, a.eps)), s.rate,
+                          w[j] * s.decay);
   }
-  const uint32_t mtop = top4(m), rtop = max(max(as_bits(r.x), as_bits(r.y)), max(as_bits(r.z), as_bits(r.w)));
+  const uint32_t mtop = as_bits(__builtin_elementwise_maximum(
+      __builtin_elementwise_maximum(__builtin_fabsf(m.x), __builtin_fabsf(m.y)),
+      __builtin_elementwise_maximum(__builtin_fabsf(m.z), __builtin_fabsf(m.w))));    // NaN stays
+  const uint32_t rtop = max(max(as_bits(r.x), as_bits(r.y)), max(as_bits(r.z), as_bits(r.w)));
   const v4u random = random_bits(s.hash + static_cast<uint32_t>(at / 4) * kHashIndex, s.key1);
   uint32_t ms, rs, mc, rc;
   if (__builtin_expect(__any(max(mtop, rtop) >= kInf), 0)) {
+    const v4f gg = g * s.gs;
+    m = decode4(q.mc, q.ms) * a.beta1 + gg * a.one_minus_beta1;
     v = decode4(q.rc, q.rs);
-    v = (v * v) * a.beta2 + (g * g) * a.one_minus_beta2;
+    v = (v * v) * a.beta2 + (gg * gg) * a.one_minus_beta2;
     w = widen(q.w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -493,27 +506,29 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
   store_codes<FULL>(t.avg, i, left, mc);
   store_codes<FULL>(t.second, i, left, rc);
   if ((threadIdx.x & 15) == 0 && (FULL || left > 0)) {
-    G<uint8_t>(t.avg_scale)[static_cast<uint32_t>(i) / static_cast<uint32_t>(kStateBlock)] = static_cast<uint8_t>(ms);
-    G<uint8_t>(t.root_scale)[static_cast<uint32_t>(i) / static_cast<uint32_t>(kStateBlock)] = static_cast<uint8_t>(rs);
+    G<uint8_t>(t.avg_scale)[static_cast<uint32_t>(i) / kStateBlock] = static_cast<uint8_t>(ms);
+    G<uint8_t>(t.root_scale)[static_cast<uint32_t>(i) / kStateBlock] = static_cast<uint8_t>(rs);
   }
 }
 
 // How a step is cut into workgroups; none of them loops.
 //
 // 32-bit states are bound by HBM (28 bytes and some 45 instructions an
-// element). One wave and 256 elements per workgroup, 16
-// workgroups per CU (each reserves 1/16 of the LDS, which the kernel does not
-// use): the accesses of the whole GPU then move through every array in step.
-// BERT-large, fp32: 1.454 ms (6.45 TB/s) against 1.55 with workgroups of 256
-// threads at the same waves per CU, 1.52 without the limit, 1.57 at 8 per CU,
-// 1.61 with two groups per lane; with workgroups of 256 threads that loop over
-// 4096 elements, 1.68; with plain loads and stores, 1.79.
+// element). One wave and 256 elements per workgroup, 16 workgroups per CU
+// (each reserves 1/16 of the LDS, which the kernel does not use): the accesses
+// of the whole GPU then move through every array in step. BERT-large, fp32:
+// 1.454 ms (6.45 TB/s) against 1.55 with workgroups of 256 threads at the same
+// waves per CU, 1.52 without the limit, 1.57 at 8 per CU, 1.61 with two groups
+// per lane; with workgroups of 256 threads that loop over 4096 elements, 1.68;
+// with plain loads and stores, 1.79.
 //
-// 8-bit states are bound by instructions as much as by HBM (16 bytes and some
-// 60 issue slots an element in fp32, 10 in bf16): full occupancy, workgroups
-// of 256 threads, since each costs a start. Where the parameters are 16-bit
-// and have no master, two groups per lane: BERT-large 0.563 ms against 0.592
-// with one; with fp32 parameters one: 0.858 ms against 0.905.
+// 8-bit states are bound by instructions nearly as much as by HBM (16 bytes
+// and some 44 instructions an element with fp32 parameters, 10 bytes in bf16):
+// the eight waves per SIMD that 64 registers allow, in workgroups of 256
+// threads, since each workgroup costs a start. Where the parameters are 16-bit
+// and have no master, two groups per lane: BERT-large 0.555 ms (6.1 TB/s)
+// against 0.592 with one, 0.566 with 7 waves; with fp32 parameters one: 0.857
+// ms (6.3 TB/s) against 0.905 with two, 0.875 with 7 waves.
 template <int PD, bool MASTER, bool F8>
 struct Shape {
   static constexpr int kThreads = F8 ? 256 : 64;
@@ -521,11 +536,12 @@ struct Shape {
   static constexpr int kPart = 4 * kThreads * kU;          // elements per workgroup
   static constexpr int kParts = kOptimTile / kPart;
   static constexpr int kLds = F8 ? 0 : 160 * 1024 / 16;
+  static constexpr int kWaves = F8 ? 8 : 1;                // per SIMD, at least
   static_assert(kParts * kPart == kOptimTile, "a tile is a whole number of parts");
 };
 
 template <int PD, int GD, bool MASTER, bool F8>
-__global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads)) void adamw_kernel(const AdamwArgs a) {
+__global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads), (Shape<PD, MASTER, F8>::kWaves)) void adamw_kernel(const AdamwArgs a) {
   constexpr int SD = MASTER ? kF32 : PD;
   typedef Shape<PD, MASTER, F8> S;
   constexpr int U = S::kU, kStep = 4 * S::kThreads;
@@ -535,6 +551,8 @@ __global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads)) void adamw_kerne
     if (a.clip->skip) return;            // every workgroup alike: the step does not count
     s.gs *= a.clip->coef;
   }
+  s.gm = a.one_minus_beta1 * s.gs;
+  s.gv = a.one_minus_beta2 * s.gs * s.gs * 0x1p64f;
   const StepScalars sc = constant(a.scalars);
   s.inv_rbc2 = sc.inv_rbc2;
   s.key0 = sc.key0;

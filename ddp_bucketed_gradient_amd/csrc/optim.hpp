@@ -23,7 +23,7 @@ enum DType : int32_t { kF32 = 0, kBF16 = 1, kF16 = 2 };
 constexpr int64_t dtype_size(int32_t d) { return d == kF32 ? 4 : 2; }
 
 // Elements that share the scale of an 8-bit state.
-constexpr int64_t kStateBlock = 64;
+constexpr uint32_t kStateBlock = 64;
 // Elements per tile, the entry of AdamW's table (96 bytes, so 0.02 an element);
 // tiles start on block boundaries and several workgroups share one.
 constexpr int64_t kOptimTile = 4096;

@@ -427,7 +427,7 @@ int ddpb_norm_bind(ddpb_norm_t n, void* const* grads, void* workspace, int64_t w
 int ddpb_norm_compute(ddpb_norm_t n, ddpb_t h, double max_norm, double grad_scale, int32_t flags);
 
 /* AdamW over P variables. With t the number of the step, per element, in fp32
- * with one rounding per operation:
+ * with at most one rounding per operation (DDPB_STATE_F32: exactly one):
  *   g' = g * (grad_scale * coef)
  *   m  = beta1 m + (1 - beta1) g'
  *   v  = beta2 v + (1 - beta2) g' g'            r = sqrt(v)

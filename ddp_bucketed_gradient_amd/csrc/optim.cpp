@@ -172,13 +172,14 @@ int64_t Adamw::workspace_bytes() const {
 
 int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes, void* stream, const Reducer* red,
                 std::string* err) {
+  if (ntiles() > kMaxTiles) {
+    *err = "adamw bind: " + std::to_string(ntiles()) + " tiles of " + std::to_string(kOptimTile) +
+           " elements, one launch takes " + std::to_string(kMaxTiles) + "; split the variables over several handles";
+    return kErrArg;
+  }
   if (const int rc = check_workspace(ws, ws_bytes, workspace_bytes(), "adamw bind", err); rc != kOk) return rc;
   if (done < 0) {
     *err = "adamw bind: negative step";
-    return kErrArg;
-  }
-  if (ntiles() > INT32_MAX) {
-    *err = "adamw bind: too many elements";
     return kErrArg;
   }
   const size_t P = c_.numel.size();

@@ -27,6 +27,8 @@ constexpr uint32_t kStateBlock = 64;
 // Elements per tile, the entry of AdamW's table (96 bytes, so 0.02 an element);
 // tiles start on block boundaries and several workgroups share one.
 constexpr int64_t kOptimTile = 4096;
+// A launch has fewer than 2^32 threads, one for four elements of each tile.
+constexpr int64_t kMaxTiles = (int64_t(1) << 32) / (kOptimTile / 4) - 1;
 // The norm's tiles, and its workgroups, each of which leaves one partial sum:
 // constants, so that the order of the sum does not depend on the device.
 constexpr int64_t kNormTileBytes = 16384;

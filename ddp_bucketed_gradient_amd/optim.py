@@ -56,6 +56,9 @@ class _Handle:
         self.stream = stream if stream is not None else torch.cuda.current_stream(device)
         if self.stream.device != device:
             raise ValueError(f"the stream belongs to {self.stream.device}, the tensors to {device}")
+        # what the caller has enqueued on the tensors so far comes first
+        if not torch.cuda.is_current_stream_capturing():
+            self.stream.wait_stream(torch.cuda.current_stream(device))
         # allocated for the stream that uses it, so that freeing it needs no wait
         with torch.cuda.device(device), torch.cuda.stream(self.stream):
             self.workspace = torch.empty(self._workspace_bytes(), dtype=torch.uint8, device=device)

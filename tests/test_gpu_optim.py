@@ -314,6 +314,34 @@ def test_special_gradients(p, state):
         assert np.isfinite(f64(c.opt.exp_avg[9])[~bad]).all()
 
 
+@pytest.mark.parametrize("g", ["f32", "f16"])
+def test_codes_beside_special_gradients(g):
+    """In the waves that hold infinities, NaN and values whose 2^64 v leaves fp32,
+    every other element gets the codes and scales it would get alone."""
+    c = Case("f32", g, "f8", seed=13, step=3)
+    c.new_grads()
+    big = c.grads[9]
+    for i, x in {0: math.inf, 63: -math.inf, 64: math.nan, 200: 0.0, 201: -0.0, 300: 1e18 if g == "f32" else 6e4,
+                 1024: math.nan, 5000: -math.inf, 12344: math.nan}.items():
+        big[i] = x
+    c.opt.exp_avg[10].view(torch.uint8)[5] = 0x7F       # a state that is NaN already, its root is not
+    big[8192:8256] = math.inf                          # a block without a finite value
+    before = c.host()
+    c.opt.step(lr=1e-3)
+    torch.cuda.synchronize()
+    for v in (9, 10):
+        n = c.numels[v]
+        (w, m, vv, r), (bw, bm, bv, br) = OO.adamw(before["w"][v], before["g"][v], before["m"][v], before["v"][v], t=4,
+                                                   lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
+                                                   gscale=1.0)
+        um, ur = OO.random16(0, 4, OO.bases(c.numels)[v] + np.arange(n, dtype=np.uint64))
+        check_codes(m, bm, um, False, raw(c.opt.exp_avg[v]), raw(c.opt.avg_scale[v]), f"m {v}")
+        check_codes(r, br, ur, True, raw(c.opt.exp_avg_root[v]), raw(c.opt.root_scale[v]), f"r {v}")
+        fine = np.isfinite(w)
+        close(f64(c.opt.params[0][v])[fine], w[fine], bw[fine], f"param {v}")
+        assert not np.isfinite(f64(c.opt.params[0][v])[~fine]).any()
+
+
 def test_same_bits_every_time():
     outs = []
     for _ in range(2):
@@ -516,6 +544,51 @@ def test_work_runs_on_the_bound_stream():
     twin.check_step(before, 1e-2, 1.0, "twin")
     for k in c.stores:
         assert np.array_equal(c.stores[k].bytes.cpu().numpy(), twin.stores[k].bytes.cpu().numpy()), k
+
+
+def test_two_handles_on_two_streams():
+    """Norm and step of two models at once, each on its own stream: what each
+    gives alone."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = []
+    for k, st in enumerate(streams):
+        with torch.cuda.stream(st):
+            c = Case("f32", "bf16", "f8" if k else "f32", seed=70 + k, stream=st)
+            both.append((c, D.GradNorm(c.grads, stream=st)))
+    twins = [(c, D.GradNorm(c.grads)) for c in (Case("f32", "bf16", "f8" if k else "f32", seed=70 + k)
+                                                for k in range(2))]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (c, n), st in zip(both, streams):
+            with torch.cuda.stream(st):
+                c.new_grads()
+                n.compute(max_norm=0.02)
+                c.opt.step(lr=1e-2, clip=n)
+    torch.cuda.synchronize()
+    for c, n in twins:
+        for _ in range(5):
+            c.new_grads()
+            n.compute(max_norm=0.02)
+            c.opt.step(lr=1e-2, clip=n)
+            torch.cuda.synchronize()
+    for (c, _), (d, _) in zip(both, twins):
+        for k in c.stores:
+            assert np.array_equal(c.stores[k].bytes.cpu().numpy(), d.stores[k].bytes.cpu().numpy()), k
+
+
+def test_masters_are_made_from_what_the_caller_enqueued():
+    side = torch.cuda.Stream()
+    p = [torch.zeros(100000, dtype=torch.bfloat16, device="cuda")]
+    g = [torch.zeros(100000, device="cuda")]
+    x = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        x = x @ x * 1e-3                                  # keeps the current stream busy
+    p[0].fill_(0.75)
+    opt = D.AdamW(p, g, master=True, stream=side, lr=0.0)
+    opt.step()
+    side.synchronize()
+    assert (opt.master[0] == 0.75).all().item() and (p[0] == 0.75).all().item()
 
 
 def test_set_step():

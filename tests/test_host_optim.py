@@ -158,6 +158,21 @@ def test_memory_named_twice_is_refused(host):
     host.adamw_destroy(a)
 
 
+def test_more_tiles_than_one_launch_takes(host):
+    """2^22 - 1 tiles of 4096 elements; the workspace of the largest is not asked for."""
+    for numel, ok in (([((1 << 22) - 1) * 4096], True), ([((1 << 22) - 1) * 4096 + 1], False),
+                      ([1, ((1 << 22) - 2) * 4096 + 1], False)):
+        a = host.adamw_create(**{**GOOD, "numel": numel, "weight_decay": None})
+        at = lambda k: [(k * 8 + i + 1) << 44 for i in range(len(numel))]  # noqa: E731
+        bind = lambda: host.adamw_bind(a, at(0) + at(1), at(2), None, at(3), at(4), None, None, 0,  # noqa: E731
+                                       1 << 30, 1 << 29, 0)
+        if ok:
+            bind()
+        else:
+            assert _code(bind) == D.E_ARG
+        host.adamw_destroy(a)
+
+
 def test_adamw_of_nothing(host):
     a = host.adamw_create(**{**GOOD, "numel": [], "weight_decay": None})
     host.adamw_bind(a, [], [], None, [], [], None, None, 0, 1 << 30, 1 << 20, 0)

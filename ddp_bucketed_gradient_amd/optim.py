@@ -8,6 +8,7 @@ tensors they were given; these must keep their storage (no resize or set_).
 from __future__ import annotations
 
 import sys as _sys
+from numbers import Real as _Real
 from typing import Optional, Sequence, Union
 
 from . import _abi
@@ -30,13 +31,23 @@ def _code(dtype, what: str) -> int:
     return c
 
 
+def _device(ts, what: str):
+    """The device of a list of tensors: the first one's, which is a GPU."""
+    import torch
+    if not ts:
+        return torch.device("cuda", torch.cuda.current_device())
+    if ts[0] is None or not ts[0].is_cuda:
+        raise ValueError(f"{what}[0] must be a CUDA tensor")
+    return ts[0].device
+
+
 def _check(ts, what: str, numels, dtype, device) -> list:
     """Addresses of contiguous CUDA tensors of one dtype and device."""
     if len(ts) != len(numels):
         raise ValueError(f"{what}: {len(ts)} tensors for {len(numels)} variables")
     ptrs = []
     for v, (t, n) in enumerate(zip(ts, numels)):
-        if t.dtype != dtype or not t.is_cuda or t.device != device or not t.is_contiguous() or t.numel() != n:
+        if t is None or t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() != n:
             raise ValueError(f"{what}[{v}] must be a contiguous {dtype} CUDA tensor of {n} elements on {device}")
         ptrs.append(t.data_ptr())
     return ptrs
@@ -102,10 +113,12 @@ class GradNorm(_Handle):
         self.h = None
         lib = lib if lib is not None else _abi.lib()
         grads = list(grads)
-        dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+        dev = _device(grads, "grads")
         ptrs = []
         for v, t in enumerate(grads):
-            ptrs += _check([t], f"grads[{v}]", [t.numel()], t.dtype, dev)
+            if t is None or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"grads[{v}] must be a contiguous CUDA tensor on {dev}")
+            ptrs.append(t.data_ptr())
         h = lib.norm_create([t.numel() for t in grads], [_code(t.dtype, "gradients") for t in grads])
         self._open(lib, h, dev, stream, reducer)
         self._keep = grads
@@ -157,20 +170,22 @@ class AdamW(_Handle):
         import torch
         self.h = None
         lib = lib if lib is not None else _abi.lib()
-        grads = list(grads)
-        rows = [list(r) for r in params] if len(params) and isinstance(params[0], (list, tuple)) else [list(params)]
+        params, grads = list(params), list(grads)
+        rows = [list(r) for r in params] if params and isinstance(params[0], (list, tuple)) else [params]
         P = len(grads)
         if state not in ("f32", "f8"):
             raise ValueError('state must be "f32" or "f8"')
         f8 = state == "f8"
-        dev = grads[0].device if P else torch.device("cuda", torch.cuda.current_device())
+        dev = _device(grads, "grads")
+        if any(t is None for ts in [grads] + rows for t in ts):
+            raise ValueError("every variable needs a parameter and a gradient tensor")
         numel = [t.numel() for t in grads]
         pt = rows[0][0].dtype if P and rows[0] else torch.float32
         gt = grads[0].dtype if P else torch.float32
         pc, gc = _code(pt, "parameters"), _code(gt, "gradients")
         pp = [a for r, row in enumerate(rows) for a in _check(row, f"params[{r}]", numel, pt, dev)]
         gp = _check(grads, "grads", numel, gt, dev)
-        every = lambda x: [float(x)] * P if isinstance(x, (int, float)) else [float(y) for y in x]  # noqa: E731
+        every = lambda x: [float(x)] * P if isinstance(x, _Real) else [float(y) for y in x]  # noqa: E731
         h = lib.adamw_create(numel, len(rows), pc, gc, _abi.STATE_F8 if f8 else _abi.STATE_F32,
                              _abi.ADAMW_MASTER if master is not None and master is not False else 0,
                              float(betas[0]), float(betas[1]), float(eps), every(weight_decay),
@@ -181,7 +196,7 @@ class AdamW(_Handle):
             if master is True:
                 self.master = self._flat(numel, torch.float32)
                 for w, p in zip(self.master, rows[0]):
-                    w.copy_(p.reshape(-1))
+                    w.copy_(p.detach().reshape(-1))
             elif master is not None and master is not False:
                 self.master = list(master)
             blocks = [-(-n // _abi.STATE_BLOCK) for n in numel]
@@ -227,9 +242,9 @@ class AdamW(_Handle):
         GradNorm on the same stream whose compute() was called before."""
         lr = self.lr if lr is None else lr
         at = 0
-        if not isinstance(lr, (int, float)):
+        if type(lr) is not float and not isinstance(lr, _Real):
             import torch
-            if lr.dtype != torch.float32 or not lr.is_cuda or lr.device != self.device or lr.numel() != 1:
+            if not isinstance(lr, torch.Tensor) or lr.dtype != torch.float32 or not lr.is_cuda or lr.device != self.device or lr.numel() != 1:
                 raise ValueError("lr must be a number or a 1-element fp32 CUDA tensor on the parameters' device")
             at, lr = lr.data_ptr(), 0.0
         result = 0
@@ -238,6 +253,13 @@ class AdamW(_Handle):
                 raise ValueError("clip must run on the same stream as the step")
             result = clip._result
         self.lib.adamw_step(self.h, lr, at, grad_scale, result, self._red())
+
+    @property
+    def states(self) -> dict:
+        """The state's tensors, as the argument ``states`` takes them: to save,
+        or to go on with in a new AdamW (with ``step=old.steps_done``) when
+        gradients or parameters have moved. It continues bit for bit."""
+        return {k: list(v) for k, v in self._state.items()}
 
     @property
     def steps_done(self) -> int:

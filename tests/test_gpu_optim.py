@@ -417,6 +417,19 @@ def test_norm_matches_the_oracle(numels, types):
         assert n.skipped.item() == 0
 
 
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("lead,gap", [(1, 0), (3, 1), (5, 7)])
+def test_norm_at_odd_addresses(t, lead, gap):
+    """Guard bytes around the tensors (0x5A5A...: large or small numbers, never
+    0) would show in the sum."""
+    s = Storage(NUMELS, TYPES[t], lead, gap)
+    for x, y in zip(s.tensors, _grads(NUMELS, [t], lead)):
+        x.copy_(y)
+    n = D.GradNorm(s.tensors)
+    want = OO.norm([f64(x) for x in s.tensors])
+    assert abs(n.compute().item() - want) <= (OO.U + sum(NUMELS) * 2.0 ** -53) * want
+
+
 def test_norm_of_values_whose_squares_leave_fp32():
     n = D.GradNorm([torch.full((10000,), 1e30, device="cuda"), torch.full((3,), 1e-30, device="cuda")])
     assert n.compute().item() == pytest.approx(1e32, rel=2e-7)
@@ -591,6 +604,41 @@ def test_masters_are_made_from_what_the_caller_enqueued():
     assert (opt.master[0] == 0.75).all().item() and (p[0] == 0.75).all().item()
 
 
+@pytest.mark.parametrize("state", ["f32", "f8"])
+def test_a_new_handle_goes_on_bit_for_bit(state):
+    a, b = (Case("bf16", "f32", state, master=True, seed=65, step=9) for _ in range(2))
+    for rep in range(4):
+        for c in (a, b):
+            c.new_grads()
+        a.opt.step(lr=1e-2)
+        b.opt.step(lr=1e-2)
+        old = b.opt
+        b.opt = D.AdamW(old.params[0], old.grads, state=state, master=old.master, states=old.states,
+                        step=old.steps_done, weight_decay=0.01)
+        old.close()
+    torch.cuda.synchronize()
+    assert a.opt.steps_done == b.opt.steps_done == 13
+    for k in a.stores:
+        assert np.array_equal(a.stores[k].bytes.cpu().numpy(), b.stores[k].bytes.cpu().numpy()), k
+
+
+def test_a_modules_parameters():
+    """nn.Module.parameters(), gradients of autograd, a NumPy rate; one step of
+    torch's arithmetic in fp64."""
+    torch.manual_seed(3)
+    m = torch.nn.Sequential(torch.nn.Linear(33, 70), torch.nn.GELU(), torch.nn.Linear(70, 5)).cuda()
+    m(torch.randn(16, 33, device="cuda")).square().mean().backward()
+    old = [f64(p) for p in m.parameters()]
+    opt = D.AdamW(m.parameters(), [p.grad for p in m.parameters()], weight_decay=0.1)
+    opt.step(lr=np.float32(0.25))
+    for p, w0 in zip(m.parameters(), old):
+        (w, *_), (bw, *_) = OO.adamw(w0, f64(p.grad), 0 * w0, 0 * w0, t=1, lr=0.25, beta1=0.9, beta2=0.999, eps=1e-8,
+                                     weight_decay=0.1, gscale=1.0)
+        close(f64(p), w, bw, "module")
+    opt = D.AdamW(list(m.bfloat16().parameters()), [p.grad.float() for p in m.parameters()], master=True)
+    assert not any(w.requires_grad for w in opt.master)
+
+
 def test_set_step():
     c = Case("f32", "f32", "f8", seed=61, step=5)
     c.opt.steps_done = 100000
@@ -615,6 +663,8 @@ def test_python_refusals():
         lambda: D.AdamW([f()], [f()], states={"exp_avg": [f()], "exp_avg_sq": [f(9)]}),
         lambda: D.AdamW([f(10, torch.bfloat16)], [f()], master=[f(10, torch.bfloat16)]),
         lambda: D.AdamW([f()], [f()], weight_decay=[0.1, 0.1]), lambda: D.GradNorm([f().cpu()]),
+        lambda: D.AdamW([f(), f()], [f(), None]), lambda: D.AdamW([f()], [None]), lambda: D.GradNorm([f(), None]),
+        lambda: D.AdamW([f()], [f().cpu()]), lambda: D.AdamW([f(), None], [f(), f()]),
         lambda: D.GradNorm([f(10, torch.int32)]), lambda: D.GradNorm([f(20)[::2]]),
     ]
     for k, call in enumerate(bad):
@@ -628,7 +678,7 @@ def test_python_refusals():
         D.AdamW([f()], [f()], master=True)                 # fp32 parameters need no master
     opt = D.AdamW([f()], [f()])
     side = torch.cuda.Stream()
-    for kw in (dict(lr=torch.ones(1)), dict(lr=f(2)), dict(lr=f(1, torch.bfloat16)),
+    for kw in (dict(lr="1e-3"), dict(lr=torch.ones(1)), dict(lr=f(2)), dict(lr=f(1, torch.bfloat16)),
                dict(clip=D.GradNorm([f()], stream=side))):
         with pytest.raises(ValueError):
             opt.step(**kw)

@@ -47,26 +47,50 @@ def kernel_source_hash() -> str:
     return h.hexdigest()[:16]
 
 
-def device_code_hash(lib_path: Optional[str] = None) -> Optional[str]:
-    """sha256 prefix of the gfx950 device code in the built library (its
-    `.hip_fatbin` section): it changes exactly when a kernel's compiled code
-    changes, not when only host code does. None if the library is missing."""
+def _elf_sections(d: bytes) -> dict:
+    """Name -> contents of a 64-bit ELF file's sections (b"" for those without
+    any); {} if it is none."""
     import struct
-    path = lib_path or os.path.join(ROOT, "ddp_bucketed_gradient_amd", "lib", "libddpb.so")
-    if not os.path.exists(path):
-        return None
-    with open(path, "rb") as f:
-        d = f.read()
     if d[:4] != b"\x7fELF" or d[4] != 2:
-        return None
+        return {}
     shoff = struct.unpack_from("<Q", d, 0x28)[0]
     shentsize, shnum, shstrndx = struct.unpack_from("<HHH", d, 0x3A)
     secs = [struct.unpack_from("<IIQQQQIIQQ", d, shoff + i * shentsize) for i in range(shnum)]
     stroff = secs[shstrndx][4]
-    for sec in secs:
-        name = d[stroff + sec[0]:d.index(b"\0", stroff + sec[0])]
-        if name == b".hip_fatbin":
-            return hashlib.sha256(d[sec[4]:sec[4] + sec[5]]).hexdigest()[:16]
+    return {d[stroff + s[0]:d.index(b"\0", stroff + s[0])]: d[s[4]:s[4] + s[5]] if s[1] != 8 else b""
+            for s in secs}
+
+
+def _code_objects(fatbin: bytes) -> List[bytes]:
+    """The gfx950 code objects in a `.hip_fatbin` section, one for each source."""
+    import struct
+    out = []
+    for m in re.finditer(b"__CLANG_OFFLOAD_BUNDLE__", fatbin):
+        at = m.start()
+        off = at + 32
+        for _ in range(struct.unpack_from("<Q", fatbin, at + 24)[0]):
+            start, size, n = struct.unpack_from("<QQQ", fatbin, off)
+            if b"gfx950" in fatbin[off + 24:off + 24 + n]:
+                out.append(fatbin[at + start:at + start + size])
+            off += 24 + n
+    return out
+
+
+def device_code_hash(lib_path: Optional[str] = None) -> Optional[str]:
+    """sha256 prefix of the reduction kernels' gfx950 machine code and kernel
+    descriptors in the built library: `.text` and `.rodata` of the code object
+    that holds them. It changes exactly when their compiled code changes, not
+    with host code, other kernels of the library or the names that the compiler
+    makes up for each build. None if the library is missing."""
+    path = lib_path or os.path.join(ROOT, "ddp_bucketed_gradient_amd", "lib", "libddpb.so")
+    if not os.path.exists(path):
+        return None
+    with open(path, "rb") as f:
+        fatbin = _elf_sections(f.read()).get(b".hip_fatbin", b"")
+    for obj in _code_objects(fatbin):
+        if b"fused_mean_kernel" in obj:
+            s = _elf_sections(obj)
+            return hashlib.sha256(s[b".text"] + s[b".rodata"]).hexdigest()[:16]
     return None
 
 

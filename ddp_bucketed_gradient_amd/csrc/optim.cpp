@@ -153,7 +153,7 @@ int Norm::compute(const Reducer* red, double max_norm, double grad_scale, bool s
 }
 
 // ---------------------------------------------------------------------------
-// AdamW: [scalars, 256 bytes][counters][tiles][replica pointers]
+// AdamW: [scalars, 256 bytes][counters][tiles][variables][replica pointers]
 
 namespace {
 constexpr int64_t kTilesAt = 256 + (kArriveBytes + 255) / 256 * 256;
@@ -165,9 +165,14 @@ int64_t Adamw::ntiles() const {
   return n;
 }
 
+int64_t Adamw::vars_at() const { return kTilesAt + up256(ntiles() * static_cast<int64_t>(sizeof(AdamwTile))); }
+
+int64_t Adamw::replicas_at() const {
+  return vars_at() + up256(static_cast<int64_t>(c_.numel.size() * sizeof(AdamwVar)));
+}
+
 int64_t Adamw::workspace_bytes() const {
-  return kTilesAt + up256(ntiles() * static_cast<int64_t>(sizeof(AdamwTile))) +
-         up256(static_cast<int64_t>(c_.R - 1) * static_cast<int64_t>(c_.numel.size()) * 8);
+  return replicas_at() + up256(static_cast<int64_t>(c_.R - 1) * static_cast<int64_t>(c_.numel.size()) * 8);
 }
 
 int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes, void* stream, const Reducer* red,
@@ -186,8 +191,8 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
   const int64_t ps = dtype_size(c_.param_dtype), gs = dtype_size(c_.grad_dtype), ss = c_.f8 ? 1 : 4;
   std::vector<char> h(static_cast<size_t>(workspace_bytes()), 0);
   AdamwTile* t = reinterpret_cast<AdamwTile*>(h.data() + kTilesAt);
-  const int64_t rep_at = kTilesAt + up256(ntiles() * static_cast<int64_t>(sizeof(AdamwTile)));
-  uint64_t* rep = reinterpret_cast<uint64_t*>(h.data() + rep_at);
+  AdamwVar* vars = reinterpret_cast<AdamwVar*>(h.data() + vars_at());
+  uint64_t* rep = reinterpret_cast<uint64_t*>(h.data() + replicas_at());
   std::vector<Range> ranges;
   ranges.reserve(P * static_cast<size_t>(c_.R + 7) + 1);
   ranges.push_back(Range{addr(ws), addr(ws) + static_cast<uint64_t>(workspace_bytes()), true});
@@ -218,25 +223,21 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
       *err = "adamw bind: NULL or misaligned pointer";
       return kErrArg;
     }
-    for (int64_t s = 0; s < n; s += kOptimTile) {
-      AdamwTile x{};
-      x.out = addr(b.params[v]) + static_cast<uint64_t>(s * ps);
-      x.src = c_.master ? addr(b.master[v]) + static_cast<uint64_t>(s * 4) : x.out;
-      x.grad = addr(b.grads[v]) + static_cast<uint64_t>(s * gs);
-      x.avg = addr(b.avg[v]) + static_cast<uint64_t>(s * ss);
-      x.second = addr(b.second[v]) + static_cast<uint64_t>(s * ss);
-      if (c_.f8) {
-        x.avg_scale = addr(b.avg_scale[v]) + static_cast<uint64_t>(s) / kStateBlock;
-        x.root_scale = addr(b.root_scale[v]) + static_cast<uint64_t>(s) / kStateBlock;
-      }
-      x.len = static_cast<int32_t>(std::min(kOptimTile, n - s));
-      x.var = static_cast<int32_t>(v);
-      x.start = s;
-      x.group0 = (base + static_cast<uint64_t>(s)) / 4;
-      x.weight_decay = c_.weight_decay.empty() ? 0.0 : c_.weight_decay[v];
-      x.lr_scale = c_.lr_scale.empty() ? 1.0 : c_.lr_scale[v];
-      *t++ = x;
+    AdamwVar& x = vars[v];
+    x.out = addr(b.params[v]);
+    x.src = c_.master ? addr(b.master[v]) : x.out;
+    x.grad = addr(b.grads[v]);
+    x.avg = addr(b.avg[v]);
+    x.second = addr(b.second[v]);
+    if (c_.f8) {
+      x.avg_scale = addr(b.avg_scale[v]);
+      x.root_scale = addr(b.root_scale[v]);
     }
+    x.group0 = base / 4;
+    x.weight_decay = c_.weight_decay.empty() ? 0.0 : c_.weight_decay[v];
+    x.lr_scale = c_.lr_scale.empty() ? 1.0 : c_.lr_scale[v];
+    for (int64_t s = 0; s < n; s += kOptimTile)
+      *t++ = AdamwTile{static_cast<int32_t>(v), static_cast<int32_t>(std::min(kOptimTile, n - s)), s};
     base += static_cast<uint64_t>(blocks * kStateBlock);
   }
   if (const int rc = check_overlap(&ranges, err); rc != kOk) return rc;
@@ -253,8 +254,9 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
   l.scalars = reinterpret_cast<StepScalars*>(dev);
   l.arrived = reinterpret_cast<uint32_t*>(dev + 256);
   l.tiles = reinterpret_cast<const AdamwTile*>(dev + kTilesAt);
+  l.vars = reinterpret_cast<const AdamwVar*>(dev + vars_at());
   l.ntiles = static_cast<int32_t>(ntiles());
-  l.replicas = reinterpret_cast<const uint64_t*>(dev + rep_at);
+  l.replicas = reinterpret_cast<const uint64_t*>(dev + replicas_at());
   l.R = c_.R;
   l.P = static_cast<int32_t>(P);
   l.beta1 = c_.beta1;

@@ -386,6 +386,7 @@ __device__ __forceinline__ float fast_div(float x, float d) {
 
 struct AdamwArgs {
   const AdamwTile* tiles;
+  const AdamwVar* vars;
   const uint64_t* replicas;
   StepScalars* scalars;
   uint32_t* arrived;
@@ -395,6 +396,13 @@ struct AdamwArgs {
   uint64_t seed;
   float grad_scale, beta1, beta2, one_minus_beta1, one_minus_beta2, eps;
   int32_t ntiles, R, P;
+};
+
+// A tile with its addresses.
+struct Tile {
+  uint64_t src, out, grad, avg, second, avg_scale, root_scale;
+  int64_t start;
+  int32_t len, var;
 };
 
 // What a lane reads for four elements, as stored.
@@ -407,7 +415,7 @@ struct Quad {
 };
 
 template <int SD, int GD, bool F8, bool FULL>
-__device__ __forceinline__ void load_quad(Quad<SD, GD, F8>& q, const AdamwTile& t, int i) {
+__device__ __forceinline__ void load_quad(Quad<SD, GD, F8>& q, const Tile& t, int i) {
   const int left = t.len - i;
   q.w = load4<SD, FULL>(t.src, i, left);
   q.g = load4<GD, FULL>(t.grad, i, left);
@@ -435,7 +443,7 @@ struct StepValues {      // of the step, in registers
 };
 
 template <int PD, bool MASTER, bool FULL>
-__device__ __forceinline__ void store_params(v4f w, const AdamwTile& t, int i, const AdamwArgs& a) {
+__device__ __forceinline__ void store_params(v4f w, const Tile& t, int i, const AdamwArgs& a) {
   const int left = t.len - i;
   store4<PD, FULL>(t.out, i, left, w);
   if constexpr (MASTER) store4<kF32, FULL>(t.src, i, left, w);
@@ -446,7 +454,7 @@ __device__ __forceinline__ void store_params(v4f w, const AdamwTile& t, int i, c
 }
 
 template <int PD, int GD, bool MASTER, bool FULL>
-__device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, false>& q, const AdamwTile& t, int at,
+__device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, false>& q, const Tile& t, int at,
                                             int lane4, const AdamwArgs& a, const StepValues& s) {
   const int i = at + lane4, left = t.len - i;
   const v4f g = widen(q.g) * s.gs;
@@ -466,7 +474,7 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, f
 // below the normal range that fast_sqrt needs; what then overflows (r > 4e9),
 // or is not finite, takes the way without shortcuts, its whole wave with it.
 template <int PD, int GD, bool MASTER, bool FULL>
-__device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, true>& q, const AdamwTile& t, int at,
+__device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, true>& q, const Tile& t, int at,
                                             int lane4, const AdamwArgs& a, const StepValues& s) {
   const int i = at + lane4, left = t.len - i;
   const v4f g = widen(q.g);
@@ -517,10 +525,12 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
 // element). One wave and 256 elements per workgroup, 16 workgroups per CU
 // (each reserves 1/16 of the LDS, which the kernel does not use): the accesses
 // of the whole GPU then move through every array in step. BERT-large, fp32:
-// 1.454 ms (6.45 TB/s) against 1.55 with workgroups of 256 threads at the same
-// waves per CU, 1.52 without the limit, 1.57 at 8 per CU, 1.61 with two groups
-// per lane; with workgroups of 256 threads that loop over 4096 elements, 1.68;
-// with plain loads and stores, 1.79.
+// 1.45 ms (6.47 TB/s). The same kernel with 96-byte tiles that hold the
+// addresses (2 % of the reads) took 1.465; that one with workgroups of 256
+// threads at the same waves per CU 1.55, without the limit 1.52, at 8 per CU
+// 1.57, with two groups per lane 1.61, with the 16 workgroups of a tile on one
+// XCD 1.66; looping over 4096 elements 1.68, and with plain loads and stores
+// 1.79.
 //
 // 8-bit states are bound by instructions nearly as much as by HBM (16 bytes
 // and some 44 instructions an element with fp32 parameters, 10 bytes in bf16):
@@ -560,12 +570,20 @@ __global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads), (Shape<PD, MASTE
   const double lr = a.lr_device != nullptr ? static_cast<double>(*a.lr_device) : a.lr;
   const int k = blockIdx.x / S::kParts, at = blockIdx.x % S::kParts * S::kPart;
   if (k < a.ntiles) {
-    const AdamwTile t = constant(a.tiles + k);
-    s.decay = static_cast<float>(1.0 - lr * t.lr_scale * t.weight_decay);
-    s.rate = static_cast<float>(lr * t.lr_scale * sc.inv_bc1);
+    const AdamwTile e = constant(a.tiles + k);
+    const AdamwVar x = constant(a.vars + e.var);
+    constexpr uint64_t kS = sizeof(typename Elem<SD>::one), kP = sizeof(typename Elem<PD>::one),
+                       kG = sizeof(typename Elem<GD>::one), kA = F8 ? 1 : 4;
+    const uint64_t from = static_cast<uint64_t>(e.start);
+    const Tile t = {x.src + from * kS,    x.out + from * kP,    x.grad + from * kG,
+                    x.avg + from * kA,    x.second + from * kA, x.avg_scale + from / kStateBlock,
+                    x.root_scale + from / kStateBlock, e.start, e.len, e.var};
+    s.decay = static_cast<float>(1.0 - lr * x.lr_scale * x.weight_decay);
+    s.rate = static_cast<float>(lr * x.lr_scale * sc.inv_bc1);
     // Tiles start on multiples of 64, so none crosses a multiple of 2^32 groups.
-    s.hash = (static_cast<uint32_t>(t.group0) + threadIdx.x) * kHashIndex +
-             static_cast<uint32_t>(t.group0 >> 32) * kHashHigh + s.key0;
+    const uint64_t group = x.group0 + from / 4;
+    s.hash = (static_cast<uint32_t>(group) + threadIdx.x) * kHashIndex +
+             static_cast<uint32_t>(group >> 32) * kHashHigh + s.key0;
     const int i = 4 * static_cast<int>(threadIdx.x);
     if (at + S::kPart <= t.len) {
       Quad<SD, GD, F8> q[U];
@@ -577,10 +595,10 @@ __global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads), (Shape<PD, MASTE
     } else {
       // All lanes of a wave stay in the loop together (row_max), those beyond
       // the end on zeros that are not stored.
-      for (int e = at; e < min(t.len, at + S::kPart); e += kStep) {
+      for (int o = at; o < min(t.len, at + S::kPart); o += kStep) {
         Quad<SD, GD, F8> q;
-        load_quad<SD, GD, F8, false>(q, t, e + i);
-        update_quad<PD, GD, MASTER, false>(q, t, e, i, a, s);
+        load_quad<SD, GD, F8, false>(q, t, o + i);
+        update_quad<PD, GD, MASTER, false>(q, t, o, i, a, s);
       }
     }
   }
@@ -665,6 +683,7 @@ class HipOptimDevice final : public OptimDevice {
     if (!on.ok()) return no_device(err);
     AdamwArgs a;
     a.tiles = l.tiles;
+    a.vars = l.vars;
     a.replicas = l.replicas;
     a.scalars = l.scalars;
     a.arrived = l.arrived;

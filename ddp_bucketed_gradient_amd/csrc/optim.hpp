@@ -24,8 +24,8 @@ constexpr int64_t dtype_size(int32_t d) { return d == kF32 ? 4 : 2; }
 
 // Elements that share the scale of an 8-bit state.
 constexpr uint32_t kStateBlock = 64;
-// Elements per tile, the entry of AdamW's table (96 bytes, so 0.02 an element);
-// tiles start on block boundaries and several workgroups share one.
+// Elements per tile of AdamW's table; tiles start on block boundaries and
+// several workgroups share one.
 constexpr int64_t kOptimTile = 4096;
 // A launch has fewer than 2^32 threads, one for four elements of each tile.
 constexpr int64_t kMaxTiles = (int64_t(1) << 32) / (kOptimTile / 4) - 1;
@@ -48,22 +48,28 @@ struct NormTile {
 };
 static_assert(sizeof(NormTile) == 16, "tile layout is shared with the kernels");
 
+// A tile names its variable, whose record holds the addresses: all tiles of a
+// large variable share one record, which the scalar caches then hold.
 struct AdamwTile {
+  int32_t var;
+  int32_t len;        // elements
+  int64_t start;      // first element inside the variable
+};
+static_assert(sizeof(AdamwTile) == 16, "tile layout is shared with the kernels");
+
+struct AdamwVar {
   uint64_t src;       // fp32 master, or the parameter of replica 0
   uint64_t out;       // parameter of replica 0
   uint64_t grad;
   uint64_t avg;       // exp_avg: fp32, or e4m3 codes
   uint64_t second;    // exp_avg_sq: fp32, or e4m3 codes of its root
-  uint64_t avg_scale; // e8m0 scale of the tile's first block (8-bit states)
+  uint64_t avg_scale; // e8m0 scales (8-bit states)
   uint64_t root_scale;
-  int32_t len;        // elements
-  int32_t var;
-  int64_t start;      // first element inside the variable
-  uint64_t group0;    // index of the tile's first group of four elements, for the random bits
+  uint64_t group0;    // index of the first group of four elements, for the random bits
   double weight_decay;
   double lr_scale;
 };
-static_assert(sizeof(AdamwTile) == 96, "tile layout is shared with the kernels");
+static_assert(sizeof(AdamwVar) == 80, "record layout is shared with the kernels");
 
 // What a norm leaves on the device (ddpb_norm_result).
 struct NormResult {
@@ -129,6 +135,7 @@ struct AdamwLaunch {
   int device;
   int32_t param_dtype, grad_dtype, f8, master;
   const AdamwTile* tiles;
+  const AdamwVar* vars;
   int32_t ntiles;
   const uint64_t* replicas;   // (R - 1) * P parameter addresses, replica-major
   int32_t R, P;
@@ -215,6 +222,8 @@ class Adamw {
 
  private:
   int64_t ntiles() const;
+  int64_t vars_at() const;
+  int64_t replicas_at() const;
   AdamwConfig c_;
   AdamwLaunch l_{};
   ReducerTie tie_;

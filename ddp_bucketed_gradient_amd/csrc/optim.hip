@@ -436,7 +436,6 @@ __device__ __forceinline__ void load_quad(Quad<SD, GD, F8>& q, const Tile& t, in
 
 struct StepValues {      // of the step, in registers
   float gs, inv_rbc2;
-  float gm, gv;          // factors of g in m and of g^2 in 2^64 v
   uint32_t key0, key1;
   float decay, rate;     // of the tile's variable
   uint32_t hash;         // random_bits' h of the lane's first group in the tile
@@ -469,20 +468,22 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, f
   store4<kF32, FULL>(t.second, i, left, v);
 }
 
-// 8-bit states, with products that feed a sum fused into it (fewer roundings
-// and instructions than one by one). v and r are carried as 2^64 v and 2^32 r, so that no v > 0 is
-// below the normal range that fast_sqrt needs; what then overflows (r > 4e9),
-// or is not finite, takes the way without shortcuts, its whole wave with it.
+// 8-bit states. m and v are rounded operation by operation, as in the 32-bit
+// step (one rounding more or less would move a code here and there); in the
+// parameter's update products are fused into the sums they feed. v and r are
+// carried as 2^64 v and 2^32 r, so that no v > 0 is below the normal range that
+// fast_sqrt needs; what then overflows (r > 4e9), or is not finite, takes the
+// way without shortcuts, its whole wave with it.
 template <int PD, int GD, bool MASTER, bool FULL>
 __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, true>& q, const Tile& t, int at,
                                             int lane4, const AdamwArgs& a, const StepValues& s) {
   const int i = at + lane4, left = t.len - i;
-  const v4f g = widen(q.g);
-  v4f m = decode4(q.mc, q.ms), v = decode4(q.rc, min(q.rs, 222u) + 32u), w = widen(q.w), r;
+  const v4f g = widen(q.g) * s.gs;
+  const v4f m = decode4(q.mc, q.ms) * a.beta1 + g * a.one_minus_beta1;
+  v4f v = decode4(q.rc, min(q.rs, 222u) + 32u), w = widen(q.w), r;
+  v = (v * v) * a.beta2 + (g * g) * (a.one_minus_beta2 * 0x1p64f);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    m[j] = __builtin_fmaf(g[j], s.gm, m[j] * a.beta1);
-    v[j] = __builtin_fmaf(g[j] * g[j], s.gv, v[j] * v[j] * a.beta2);
     r[j] = fast_sqrt(v[j]);
     w[j] = __builtin_fmaf(-fast_div(m[j], __builtin_fmaf(r[j], s.inv_rbc2 * 0x1p-32f, a.eps)), s.rate,
                           w[j] * s.decay);
@@ -494,10 +495,8 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
   const v4u random = random_bits(s.hash + static_cast<uint32_t>(at / 4) * kHashIndex, s.key1);
   uint32_t ms, rs, mc, rc;
   if (__builtin_expect(__any(max(mtop, rtop) >= kInf), 0)) {
-    const v4f gg = g * s.gs;
-    m = decode4(q.mc, q.ms) * a.beta1 + gg * a.one_minus_beta1;
     v = decode4(q.rc, q.rs);
-    v = (v * v) * a.beta2 + (gg * gg) * a.one_minus_beta2;
+    v = (v * v) * a.beta2 + (g * g) * a.one_minus_beta2;
     w = widen(q.w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -533,12 +532,14 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
 // 1.79.
 //
 // 8-bit states are bound by instructions nearly as much as by HBM (16 bytes
-// and some 44 instructions an element with fp32 parameters, 10 bytes in bf16):
+// and some 47 instructions an element with fp32 parameters, 10 bytes in bf16):
 // the eight waves per SIMD that 64 registers allow, in workgroups of 256
 // threads, since each workgroup costs a start. Where the parameters are 16-bit
-// and have no master, two groups per lane: BERT-large 0.555 ms (6.1 TB/s)
-// against 0.592 with one, 0.566 with 7 waves; with fp32 parameters one: 0.857
-// ms (6.3 TB/s) against 0.905 with two, 0.875 with 7 waves.
+// and have no master, two groups per lane: BERT-large 0.547 ms (6.2 TB/s)
+// against 0.592 with one and 0.566 with 7 waves; with fp32 parameters one:
+// 0.857 ms (6.3 TB/s) against 0.905 with two and 0.875 with 7 waves. The
+// scales in scalar loads, or the groups of several lanes per XCD, gained
+// nothing.
 template <int PD, bool MASTER, bool F8>
 struct Shape {
   static constexpr int kThreads = F8 ? 256 : 64;
@@ -561,8 +562,6 @@ __global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads), (Shape<PD, MASTE
     if (a.clip->skip) return;            // every workgroup alike: the step does not count
     s.gs *= a.clip->coef;
   }
-  s.gm = a.one_minus_beta1 * s.gs;
-  s.gv = a.one_minus_beta2 * s.gs * s.gs * 0x1p64f;
   const StepScalars sc = constant(a.scalars);
   s.inv_rbc2 = sc.inv_rbc2;
   s.key0 = sc.key0;

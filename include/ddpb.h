@@ -395,7 +395,7 @@ int ddpb_reset(ddpb_t h);
  * compute stream.
  */
 
-/* Global norm of P tensors: norm = grad_scale * sqrt(sum of all squares),
+/* Global norm of P tensors: norm = |grad_scale| * sqrt(sum of all squares),
  * summed in fp64 in a fixed order (the same bits on every run); coef =
  * max_norm / norm where norm > max_norm, else 1. */
 typedef struct ddpb_norm* ddpb_norm_t;

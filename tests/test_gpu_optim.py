@@ -699,6 +699,35 @@ def test_nothing_to_update():
 
 # ---- a training step as it is used -------------------------------------------------------------
 
+def test_groups_share_one_norm_behind_a_sync():
+    """Matrices with 8-bit states and decay, vectors with 32-bit states and none:
+    two handles on one reducer's gradients, one coefficient for both."""
+    shapes = [(33, 31), (33,), (64, 70), (64,), (4097, 2)]
+    R, rng = 2, np.random.default_rng(8)
+    red = D.Reducer(shapes, R, 4 * 3000)
+    grads = [[torch.from_numpy(rng.normal(size=s).astype(np.float32)).cuda() for s in shapes] for _ in range(R)]
+    red.bind(grads)
+    params = [torch.from_numpy(rng.normal(size=s).astype(np.float32) * 0.02).cuda() for s in shapes]
+    big, small = [0, 2, 4], [1, 3]
+    norm = red.grad_norm()
+    opts = [D.AdamW([params[v] for v in vs], [grads[0][v] for v in vs], weight_decay=wd, state=st, reducer=red)
+            for vs, wd, st in ((big, 0.1, "f8"), (small, 0.0, "f32"))]
+    old = [f64(p) for p in params]
+    red.sync()
+    norm.compute(max_norm=0.5)
+    for o in opts:
+        o.step(lr=1e-2, clip=norm)
+    torch.cuda.synchronize()
+    g = [f64(x) for x in grads[0]]
+    coef = OO.clip_coef(OO.norm(g), 0.5)
+    assert coef < 1 and abs(norm.coef.item() - coef) <= 4 * OO.U * coef
+    for v in range(len(shapes)):
+        (w, *_), (bw, *_) = OO.adamw(old[v], g[v], 0 * g[v], 0 * g[v], t=1, lr=1e-2, beta1=0.9, beta2=0.999, eps=1e-8,
+                                     weight_decay=0.1 if v in big else 0.0, gscale=norm.coef.item())
+        close(f64(params[v]), w, bw, f"variable {v}")
+    red.close()
+
+
 @pytest.mark.parametrize("state", ["f32", "f8"])
 @pytest.mark.parametrize("view", [False, True])
 def test_synchronise_clip_and_step(view, state):

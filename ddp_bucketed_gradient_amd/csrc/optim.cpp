@@ -153,22 +153,33 @@ int Norm::compute(const Reducer* red, double max_norm, double grad_scale, bool s
 }
 
 // ---------------------------------------------------------------------------
-// AdamW: [scalars, 256 bytes][counters][tiles][variables][replica pointers]
+// AdamW: [scalars, neutral norm result, 256 bytes][counters][tiles][variables][replica pointers]
+// There is always a tile and a variable: empty ones for a step of nothing.
 
 namespace {
+constexpr int64_t kNeutralAt = 64;
 constexpr int64_t kTilesAt = 256 + (kArriveBytes + 255) / 256 * 256;
 }
 
-int64_t Adamw::ntiles() const {
+int64_t Adamw::whole() const {
   int64_t n = 0;
-  for (int64_t k : c_.numel) n += (k + kOptimTile - 1) / kOptimTile;
+  for (int64_t k : c_.numel) n += k / kOptimTile;
   return n;
 }
 
-int64_t Adamw::vars_at() const { return kTilesAt + up256(ntiles() * static_cast<int64_t>(sizeof(AdamwTile))); }
+int64_t Adamw::rests() const {
+  const int64_t part = adamw_part(c_.param_dtype, c_.master, c_.f8);
+  int64_t n = 0;
+  for (int64_t k : c_.numel) n += (k % kOptimTile + part - 1) / part;
+  return n;
+}
+
+int64_t Adamw::vars_at() const {
+  return kTilesAt + up256(std::max<int64_t>(whole() + rests(), 1) * static_cast<int64_t>(sizeof(AdamwTile)));
+}
 
 int64_t Adamw::replicas_at() const {
-  return vars_at() + up256(static_cast<int64_t>(c_.numel.size() * sizeof(AdamwVar)));
+  return vars_at() + up256(static_cast<int64_t>(std::max<size_t>(c_.numel.size(), 1) * sizeof(AdamwVar)));
 }
 
 int64_t Adamw::workspace_bytes() const {
@@ -177,9 +188,12 @@ int64_t Adamw::workspace_bytes() const {
 
 int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes, void* stream, const Reducer* red,
                 std::string* err) {
-  if (ntiles() > kMaxTiles) {
-    *err = "adamw bind: " + std::to_string(ntiles()) + " tiles of " + std::to_string(kOptimTile) +
-           " elements, one launch takes " + std::to_string(kMaxTiles) + "; split the variables over several handles";
+  const int64_t part = adamw_part(c_.param_dtype, c_.master, c_.f8);
+  const int64_t groups = whole() * (kOptimTile / part) + rests();
+  if (groups > kMaxThreads / adamw_threads(c_.f8)) {
+    *err = "adamw bind: one launch takes " + std::to_string(kMaxThreads / adamw_threads(c_.f8)) + " workgroups of " +
+           std::to_string(part) + " elements, this needs " + std::to_string(groups) +
+           "; split the variables over several handles";
     return kErrArg;
   }
   if (const int rc = check_workspace(ws, ws_bytes, workspace_bytes(), "adamw bind", err); rc != kOk) return rc;
@@ -191,6 +205,7 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
   const int64_t ps = dtype_size(c_.param_dtype), gs = dtype_size(c_.grad_dtype), ss = c_.f8 ? 1 : 4;
   std::vector<char> h(static_cast<size_t>(workspace_bytes()), 0);
   AdamwTile* t = reinterpret_cast<AdamwTile*>(h.data() + kTilesAt);
+  AdamwTile* rest = t + whole();
   AdamwVar* vars = reinterpret_cast<AdamwVar*>(h.data() + vars_at());
   uint64_t* rep = reinterpret_cast<uint64_t*>(h.data() + replicas_at());
   std::vector<Range> ranges;
@@ -236,8 +251,11 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
     x.group0 = base / 4;
     x.weight_decay = c_.weight_decay.empty() ? 0.0 : c_.weight_decay[v];
     x.lr_scale = c_.lr_scale.empty() ? 1.0 : c_.lr_scale[v];
-    for (int64_t s = 0; s < n; s += kOptimTile)
-      *t++ = AdamwTile{static_cast<int32_t>(v), static_cast<int32_t>(std::min(kOptimTile, n - s)), s};
+    int64_t s = 0;
+    for (; s + kOptimTile <= n; s += kOptimTile)
+      *t++ = AdamwTile{static_cast<int32_t>(v), static_cast<int32_t>(kOptimTile), s};
+    for (; s < n; s += part)
+      *rest++ = AdamwTile{static_cast<int32_t>(v), static_cast<int32_t>(std::min(part, n - s)), s};
     base += static_cast<uint64_t>(blocks * kStateBlock);
   }
   if (const int rc = check_overlap(&ranges, err); rc != kOk) return rc;
@@ -246,16 +264,19 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
   if (const int rc = optim_device()->current(&l.device, err); rc != kOk) return rc;
   const StepScalars sc = step_scalars(done, c_.beta1, c_.beta2, c_.seed);
   std::memcpy(h.data(), &sc, sizeof(sc));
+  reinterpret_cast<NormResult*>(h.data() + kNeutralAt)->coef = 1.0f;
   char* dev = static_cast<char*>(ws);
   l.param_dtype = c_.param_dtype;
   l.grad_dtype = c_.grad_dtype;
   l.f8 = c_.f8 ? 1 : 0;
   l.master = c_.master ? 1 : 0;
   l.scalars = reinterpret_cast<StepScalars*>(dev);
+  l.neutral = reinterpret_cast<const NormResult*>(dev + kNeutralAt);
   l.arrived = reinterpret_cast<uint32_t*>(dev + 256);
   l.tiles = reinterpret_cast<const AdamwTile*>(dev + kTilesAt);
   l.vars = reinterpret_cast<const AdamwVar*>(dev + vars_at());
-  l.ntiles = static_cast<int32_t>(ntiles());
+  l.whole = static_cast<int32_t>(whole());
+  l.rests = static_cast<int32_t>(rests());
   l.replicas = reinterpret_cast<const uint64_t*>(dev + replicas_at());
   l.R = c_.R;
   l.P = static_cast<int32_t>(P);

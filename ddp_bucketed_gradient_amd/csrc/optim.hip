@@ -395,7 +395,7 @@ struct AdamwArgs {
   double lr, beta1d, beta2d;
   uint64_t seed;
   float grad_scale, beta1, beta2, one_minus_beta1, one_minus_beta2, eps;
-  int32_t ntiles, R, P;
+  int32_t whole, rests, R, P;
 };
 
 // A tile with its addresses.
@@ -436,7 +436,7 @@ __device__ __forceinline__ void load_quad(Quad<SD, GD, F8>& q, const Tile& t, in
 
 struct StepValues {      // of the step, in registers
   float gs, inv_rbc2;
-  uint32_t key0, key1;
+  uint32_t key1;
   float decay, rate;     // of the tile's variable
   uint32_t hash;         // random_bits' h of the lane's first group in the tile
 };
@@ -521,15 +521,17 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
 // How a step is cut into workgroups; none of them loops.
 //
 // 32-bit states are bound by HBM (28 bytes and some 45 instructions an
-// element). One wave and 256 elements per workgroup, 16 workgroups per CU
-// (each reserves 1/16 of the LDS, which the kernel does not use): the accesses
-// of the whole GPU then move through every array in step. BERT-large, fp32:
-// 1.45 ms (6.47 TB/s). The same kernel with 96-byte tiles that hold the
-// addresses (2 % of the reads) took 1.465; that one with workgroups of 256
-// threads at the same waves per CU 1.55, without the limit 1.52, at 8 per CU
-// 1.57, with two groups per lane 1.61, with the 16 workgroups of a tile on one
-// XCD 1.66; looping over 4096 elements 1.68, and with plain loads and stores
-// 1.79.
+// element). One wave and 256 elements per workgroup, 13 or 16 workgroups per
+// CU (each reserves its share of the LDS, which the kernel does not use): the
+// accesses of the whole GPU then move through every array in step. 13 where a
+// workgroup reads and writes 28 bytes an element (BERT-large, fp32: 1.44 ms,
+// 6.5 TB/s, against 1.46 with 16, 1.57 with 8 and 1.52 without the limit), 16
+// where it reads less (bf16 without masters: 1.12 ms against 1.16) or mostly
+// writes (ResNet-50, 8 replicas: 0.243 ms against 0.251). Other cuts of the
+// same case: workgroups of 256 threads at the same waves per CU 1.55, two
+// groups per lane 1.61, all workgroups of a tile on one XCD 1.66, workgroups
+// of 256 threads that loop over 4096 elements 1.68, and with plain loads and
+// stores 1.79.
 //
 // 8-bit states are bound by instructions nearly as much as by HBM (16 bytes
 // and some 47 instructions an element with fp32 parameters, 10 bytes in bf16):
@@ -542,69 +544,78 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
 // nothing.
 template <int PD, bool MASTER, bool F8>
 struct Shape {
-  static constexpr int kThreads = F8 ? 256 : 64;
-  static constexpr int kU = F8 && PD != kF32 && !MASTER ? 2 : 1;
-  static constexpr int kPart = 4 * kThreads * kU;          // elements per workgroup
+  static constexpr int kThreads = adamw_threads(F8);
+  static constexpr int kU = adamw_unroll(PD, MASTER, F8);
+  static constexpr int kPart = adamw_part(PD, MASTER, F8);
   static constexpr int kParts = kOptimTile / kPart;
-  static constexpr int kLds = F8 ? 0 : 160 * 1024 / 16;
+  static int lds(int R) { return F8 ? 0 : 160 * 1024 / ((PD != kF32 && !MASTER) || R > 4 ? 16 : 13); }
   static constexpr int kWaves = F8 ? 8 : 1;                // per SIMD, at least
   static_assert(kParts * kPart == kOptimTile, "a tile is a whole number of parts");
 };
 
 template <int PD, int GD, bool MASTER, bool F8>
-__global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads), (Shape<PD, MASTER, F8>::kWaves)) void adamw_kernel(const AdamwArgs a) {
+__global__ __launch_bounds__((Shape<PD, MASTER, F8>::kThreads), (Shape<PD, MASTER, F8>::kWaves))
+void adamw_kernel(const AdamwArgs a) {
   constexpr int SD = MASTER ? kF32 : PD;
   typedef Shape<PD, MASTER, F8> S;
   constexpr int U = S::kU, kStep = 4 * S::kThreads;
-  StepValues s;
-  s.gs = a.grad_scale;
-  if (a.clip != nullptr) {
-    if (a.clip->skip) return;            // every workgroup alike: the step does not count
-    s.gs *= a.clip->coef;
-  }
+  // One of the rests (which come first: at the end, nothing would run beside
+  // them), or this workgroup's part of a whole tile.
+  const int b = static_cast<int>(blockIdx.x) - a.rests;
+  const bool rest = b < 0;
+  const uint32_t k = rest ? a.whole + static_cast<int>(blockIdx.x) : b / S::kParts;
+  const int at = rest ? 0 : b % S::kParts * S::kPart;
+  // Two scalar round trips stand before the first data: these, which do not
+  // wait for one another (there is always a norm result and a tile to read,
+  // neutral ones if need be), and the variable's record. So a step that is to
+  // be skipped is one of empty tiles, too: a branch would be a third.
+  const AdamwTile e = constant(a.tiles + k);
+  const NormResult clip = constant(a.clip);
   const StepScalars sc = constant(a.scalars);
-  s.inv_rbc2 = sc.inv_rbc2;
-  s.key0 = sc.key0;
-  s.key1 = sc.key1;
-  const double lr = a.lr_device != nullptr ? static_cast<double>(*a.lr_device) : a.lr;
-  const int k = blockIdx.x / S::kParts, at = blockIdx.x % S::kParts * S::kPart;
-  if (k < a.ntiles) {
-    const AdamwTile e = constant(a.tiles + k);
-    const AdamwVar x = constant(a.vars + e.var);
-    constexpr uint64_t kS = sizeof(typename Elem<SD>::one), kP = sizeof(typename Elem<PD>::one),
-                       kG = sizeof(typename Elem<GD>::one), kA = F8 ? 1 : 4;
-    const uint64_t from = static_cast<uint64_t>(e.start);
-    const Tile t = {x.src + from * kS,    x.out + from * kP,    x.grad + from * kG,
-                    x.avg + from * kA,    x.second + from * kA, x.avg_scale + from / kStateBlock,
-                    x.root_scale + from / kStateBlock, e.start, e.len, e.var};
+  const AdamwVar x = constant(a.vars + e.var);
+  constexpr uint64_t kS = sizeof(typename Elem<SD>::one), kP = sizeof(typename Elem<PD>::one),
+                     kG = sizeof(typename Elem<GD>::one), kA = F8 ? 1 : 4;
+  const uint64_t from = static_cast<uint64_t>(e.start);
+  const Tile t = {x.src + from * kS,    x.out + from * kP,    x.grad + from * kG,
+                  x.avg + from * kA,    x.second + from * kA, x.avg_scale + from / kStateBlock,
+                  x.root_scale + from / kStateBlock, e.start, clip.skip ? 0 : e.len, e.var};
+  const int i = 4 * static_cast<int>(threadIdx.x);
+  auto step_values = [&] {
+    StepValues s;
+    s.gs = a.grad_scale * clip.coef;
+    s.inv_rbc2 = sc.inv_rbc2;
+    s.key1 = sc.key1;
+    const double lr = a.lr_device != nullptr ? static_cast<double>(constant(a.lr_device)) : a.lr;
     s.decay = static_cast<float>(1.0 - lr * x.lr_scale * x.weight_decay);
     s.rate = static_cast<float>(lr * x.lr_scale * sc.inv_bc1);
     // Tiles start on multiples of 64, so none crosses a multiple of 2^32 groups.
     const uint64_t group = x.group0 + from / 4;
     s.hash = (static_cast<uint32_t>(group) + threadIdx.x) * kHashIndex +
-             static_cast<uint32_t>(group >> 32) * kHashHigh + s.key0;
-    const int i = 4 * static_cast<int>(threadIdx.x);
-    if (at + S::kPart <= t.len) {
-      Quad<SD, GD, F8> q[U];
+             static_cast<uint32_t>(group >> 32) * kHashHigh + sc.key0;
+    return s;
+  };
+  if (at + S::kPart <= t.len) {
+    Quad<SD, GD, F8> q[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) load_quad<SD, GD, F8, true>(q[u], t, at + kStep * u + i);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int u = 0; u < U; ++u) load_quad<SD, GD, F8, true>(q[u], t, at + kStep * u + i);
+    __builtin_amdgcn_sched_barrier(0);
+    const StepValues s = step_values();
 #pragma unroll
-      for (int u = 0; u < U; ++u) update_quad<PD, GD, MASTER, true>(q[u], t, at + kStep * u, i, a, s);
-    } else {
-      // All lanes of a wave stay in the loop together (row_max), those beyond
-      // the end on zeros that are not stored.
-      for (int o = at; o < min(t.len, at + S::kPart); o += kStep) {
-        Quad<SD, GD, F8> q;
-        load_quad<SD, GD, F8, false>(q, t, o + i);
-        update_quad<PD, GD, MASTER, false>(q, t, o, i, a, s);
-      }
+    for (int u = 0; u < U; ++u) update_quad<PD, GD, MASTER, true>(q[u], t, at + kStep * u, i, a, s);
+  } else {
+    // All lanes of a wave stay in the loop together (row_max), those beyond
+    // the end on zeros that are not stored.
+    const StepValues s = step_values();
+    for (int o = at; o < t.len; o += kStep) {
+      Quad<SD, GD, F8> q;
+      load_quad<SD, GD, F8, false>(q, t, o + i);
+      update_quad<PD, GD, MASTER, false>(q, t, o, i, a, s);
     }
   }
   // The workgroup that is done last has seen every other read the scalars: it
   // advances them for the next step.
   __syncthreads();
-  if (threadIdx.x == 0 && last_to_arrive(a.arrived))
+  if (threadIdx.x == 0 && last_to_arrive(a.arrived) && !clip.skip)
     *a.scalars = step_scalars(sc.done + 1, a.beta1d, a.beta2d, a.seed);
 }
 
@@ -633,8 +644,9 @@ class OnDevice {
 template <int PD, int GD, bool MASTER, bool F8>
 void launch_adamw(const AdamwArgs& a, hipStream_t s) {
   typedef Shape<PD, MASTER, F8> S;
-  const unsigned blocks = static_cast<unsigned>(a.ntiles > 0 ? a.ntiles : 1) * S::kParts;
-  hipLaunchKernelGGL((adamw_kernel<PD, GD, MASTER, F8>), dim3(blocks), dim3(S::kThreads), S::kLds, s, a);
+  const unsigned blocks = static_cast<unsigned>(a.whole) * S::kParts + static_cast<unsigned>(a.rests);
+  hipLaunchKernelGGL((adamw_kernel<PD, GD, MASTER, F8>), dim3(blocks > 0 ? blocks : 1), dim3(S::kThreads),
+                     S::lds(a.R), s, a);
 }
 
 template <int PD, int GD>
@@ -686,7 +698,7 @@ class HipOptimDevice final : public OptimDevice {
     a.replicas = l.replicas;
     a.scalars = l.scalars;
     a.arrived = l.arrived;
-    a.clip = l.clip;
+    a.clip = l.clip != nullptr ? l.clip : l.neutral;
     a.lr_device = l.lr_device;
     a.lr = l.lr;
     a.beta1d = l.beta1;
@@ -698,7 +710,8 @@ class HipOptimDevice final : public OptimDevice {
     a.one_minus_beta1 = static_cast<float>(1.0 - l.beta1);
     a.one_minus_beta2 = static_cast<float>(1.0 - l.beta2);
     a.eps = static_cast<float>(l.eps);
-    a.ntiles = l.ntiles;
+    a.whole = l.whole;
+    a.rests = l.rests;
     a.R = l.R;
     a.P = l.P;
     hipStream_t s = static_cast<hipStream_t>(l.stream);

@@ -24,11 +24,24 @@ constexpr int64_t dtype_size(int32_t d) { return d == kF32 ? 4 : 2; }
 
 // Elements that share the scale of an 8-bit state.
 constexpr uint32_t kStateBlock = 64;
-// Elements per tile of AdamW's table; tiles start on block boundaries and
-// several workgroups share one.
+// Elements per tile of AdamW's table; tiles start on block boundaries. The
+// workgroups of a whole tile share its entry. What is left of a variable has
+// an entry for each workgroup: with entries of whole tiles there too, 5000
+// variables of 64 elements took 49 us instead of 7, most of it workgroups
+// without work.
 constexpr int64_t kOptimTile = 4096;
-// A launch has fewer than 2^32 threads, one for four elements of each tile.
-constexpr int64_t kMaxTiles = (int64_t(1) << 32) / (kOptimTile / 4) - 1;
+
+// How a step is cut into workgroups (why so: optim.hip): threads, groups of
+// four elements per lane, elements per workgroup.
+constexpr int adamw_threads(bool f8) { return f8 ? 256 : 64; }
+constexpr int adamw_unroll(int32_t param_dtype, bool master, bool f8) {
+  return f8 && param_dtype != 0 && !master ? 2 : 1;
+}
+constexpr int64_t adamw_part(int32_t param_dtype, bool master, bool f8) {
+  return 4 * adamw_threads(f8) * adamw_unroll(param_dtype, master, f8);
+}
+// A launch has fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
 // The norm's tiles, and its workgroups, each of which leaves one partial sum:
 // constants, so that the order of the sum does not depend on the device.
 constexpr int64_t kNormTileBytes = 16384;
@@ -52,7 +65,7 @@ static_assert(sizeof(NormTile) == 16, "tile layout is shared with the kernels");
 // large variable share one record, which the scalar caches then hold.
 struct AdamwTile {
   int32_t var;
-  int32_t len;        // elements
+  int32_t len;        // elements: kOptimTile, or at most a workgroup's
   int64_t start;      // first element inside the variable
 };
 static_assert(sizeof(AdamwTile) == 16, "tile layout is shared with the kernels");
@@ -134,14 +147,15 @@ struct AdamwLaunch {
   void* stream;
   int device;
   int32_t param_dtype, grad_dtype, f8, master;
-  const AdamwTile* tiles;
+  const AdamwTile* tiles;     // whole tiles, then the rests
   const AdamwVar* vars;
-  int32_t ntiles;
+  int32_t whole, rests;
   const uint64_t* replicas;   // (R - 1) * P parameter addresses, replica-major
   int32_t R, P;
   StepScalars* scalars;
   uint32_t* arrived;          // kArriveBytes
   const NormResult* clip;     // or NULL
+  const NormResult* neutral;  // norm 0, coef 1
   const float* lr_device;     // or NULL: lr
   double lr, grad_scale;
   double beta1, beta2, eps;
@@ -221,7 +235,8 @@ class Adamw {
   const AdamwConfig& config() const { return c_; }
 
  private:
-  int64_t ntiles() const;
+  int64_t whole() const;
+  int64_t rests() const;
   int64_t vars_at() const;
   int64_t replicas_at() const;
   AdamwConfig c_;

@@ -158,14 +158,19 @@ def test_memory_named_twice_is_refused(host):
     host.adamw_destroy(a)
 
 
-def test_more_tiles_than_one_launch_takes(host):
-    """2^22 - 1 tiles of 4096 elements; the workspace of the largest is not asked for."""
-    for numel, ok in (([((1 << 22) - 1) * 4096], True), ([((1 << 22) - 1) * 4096 + 1], False),
-                      ([1, ((1 << 22) - 2) * 4096 + 1], False)):
-        a = host.adamw_create(**{**GOOD, "numel": numel, "weight_decay": None})
+@pytest.mark.parametrize("state,pd,part,threads", [(D.STATE_F32, D.F32, 256, 64), (D.STATE_F8, D.F32, 1024, 256),
+                                                   (D.STATE_F8, D.BF16, 2048, 256)])
+def test_more_workgroups_than_one_launch_takes(host, state, pd, part, threads):
+    """Fewer than 2^32 threads a launch, one workgroup for ``part`` elements or a
+    variable's rest."""
+    most = ((1 << 32) - 1) // threads
+    for numel, ok in (([most * part], True), ([most * part + 1], False), ([1, (most - 1) * part], True),
+                      ([1, (most - 1) * part + 1], False), ([1, 0, most * part], False)):
+        a = host.adamw_create(**{**GOOD, "numel": numel, "weight_decay": None, "state": state, "param_dtype": pd})
         at = lambda k: [(k * 8 + i + 1) << 44 for i in range(len(numel))]  # noqa: E731
-        bind = lambda: host.adamw_bind(a, at(0) + at(1), at(2), None, at(3), at(4), None, None, 0,  # noqa: E731
-                                       1 << 30, 1 << 29, 0)
+        sc = (at(5), at(6)) if state == D.STATE_F8 else (None, None)
+        bind = lambda: host.adamw_bind(a, at(0) + at(1), at(2), None, at(3), at(4), *sc, 0, 1 << 30,  # noqa: E731
+                                       1 << 29, 0)
         if ok:
             bind()
         else:

@@ -158,6 +158,9 @@ int Norm::compute(const Reducer* red, double max_norm, double grad_scale, bool s
 
 namespace {
 constexpr int64_t kNeutralAt = 64;
+
+// Counts of steps that leave room to count on.
+bool step_ok(int64_t done) { return done >= 0 && done <= (int64_t(1) << 53); }
 constexpr int64_t kTilesAt = 256 + (kArriveBytes + 255) / 256 * 256;
 }
 
@@ -197,8 +200,8 @@ int Adamw::bind(const AdamwBuffers& b, int64_t done, void* ws, int64_t ws_bytes,
     return kErrArg;
   }
   if (const int rc = check_workspace(ws, ws_bytes, workspace_bytes(), "adamw bind", err); rc != kOk) return rc;
-  if (done < 0) {
-    *err = "adamw bind: negative step";
+  if (!step_ok(done)) {
+    *err = "adamw bind: step out of range";
     return kErrArg;
   }
   const size_t P = c_.numel.size();
@@ -322,8 +325,8 @@ int Adamw::set_step(int64_t done, std::string* err) {
     *err = "adamw set_step: not bound";
     return kErrState;
   }
-  if (done < 0) {
-    *err = "adamw set_step: negative step";
+  if (!step_ok(done)) {
+    *err = "adamw set_step: step out of range";
     return kErrArg;
   }
   const StepScalars sc = step_scalars(done, c_.beta1, c_.beta2, c_.seed);

@@ -474,7 +474,7 @@ int ddpb_adamw_workspace_bytes(ddpb_adamw_t a, int64_t* bytes);
  *   exp_avg     P pointers: m, fp32 or codes
  *   second      P pointers: v in fp32, or codes of r
  *   avg_scale, root_scale   P pointers to ceil(numel / 64) bytes (DDPB_STATE_F8; else NULL)
- *   step        steps already done (0 for a new state, which must be all zeros)
+ *   step        steps already done, 0..2^53 (0 for a new state, which must be all zeros)
  * Every array contiguous and aligned to its element type (NULL where numel is
  * 0). The memory that a step writes must not overlap anything else named here:
  * DDPB_E_ARG for a tied parameter listed twice, and for more workgroups than

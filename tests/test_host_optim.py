@@ -120,7 +120,8 @@ def test_adamw_bind_and_step(host, state, pd, master):
     assert _code(lambda: bind(ws_bytes=host.adamw_workspace_bytes(a) - 1)) == D.E_ARG
     assert _code(lambda: bind(workspace=(1 << 30) + 64)) == D.E_ARG
     assert _code(lambda: bind(workspace=0)) == D.E_ARG
-    assert _code(lambda: bind(step=-1)) == D.E_ARG
+    for t in (-1, (1 << 53) + 1, (1 << 63) - 1):
+        assert _code(lambda: bind(step=t)) == D.E_ARG
     empty = list(good["grads"])
     empty[1] = 0                                                                       # numel 0: may be NULL
     bind(grads=empty)
@@ -130,8 +131,9 @@ def test_adamw_bind_and_step(host, state, pd, master):
         assert _code(lambda: host.adamw_step(a, lr, 0, sc)) == D.E_ARG
     assert _code(lambda: host.adamw_step(a, 1e-3, 0x1001)) == D.E_ARG
     assert _code(lambda: host.adamw_step(a, 1e-3, 0, 1.0, 0x2002)) == D.E_ARG
-    assert _code(lambda: host.adamw_set_step(a, -1)) == D.E_ARG
-    host.adamw_set_step(a, 5)
+    for t in (-1, (1 << 53) + 1, (1 << 63) - 1):
+        assert _code(lambda: host.adamw_set_step(a, t)) == D.E_ARG
+    host.adamw_set_step(a, 1 << 53)
     host.adamw_destroy(a)
 
 

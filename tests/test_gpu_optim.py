@@ -64,7 +64,7 @@ class Case:
     """Parameters, gradients and state in guarded storages, and their AdamW."""
 
     def __init__(self, p="f32", g="f32", state="f32", master=False, R=1, lead=0, gap=0, numels=NUMELS, seed=1,
-                 zero=False, **opt):
+                 zero=False, random_seed=0, **opt):
         self.numels, self.p, self.g, self.f8, self.R = numels, p, g, state == "f8", R
         self.stores = {}
         new = lambda name, ns, dt: self.stores.setdefault(name, Storage(ns, dt, lead, gap)).tensors  # noqa: E731
@@ -102,9 +102,10 @@ class Case:
                     t.copy_(rnd(n) * 1e-3 if k == "exp_avg" else (rnd(n) * 1e-3) ** 2)
         self.wd = opt.setdefault("weight_decay", 0.01)
         self.lr_scale = opt.get("lr_scale")
-        self.seed, self.t = opt.get("seed", 0), opt.get("step", 0)
+        self.seed, self.t = random_seed, opt.get("step", 0)
         self.eps, self.betas = opt.get("eps", 1e-8), opt.get("betas", (0.9, 0.999))
-        self.opt = D.AdamW(rows if R > 1 else rows[0], self.grads, state=state, master=ms, states=states, **opt)
+        self.opt = D.AdamW(rows if R > 1 else rows[0], self.grads, state=state, master=ms, states=states,
+                           seed=random_seed, **opt)
 
     def new_grads(self, scale=1e-3):
         for t in self.grads:
@@ -389,6 +390,40 @@ def test_tensor_beyond_32_bit_offsets():
             check_codes(x[cut], b[cut], u[cut], root, raw(codes[lo * 64:e]), raw(scales[lo:hi]), f"codes at {a}")
     rest = p[1 << 20:1 << 21]
     assert (rest == rest[0]).all().item() and abs(rest[0].item() - 0.49) <= 0.49 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_configurations(seed):
+    """Types, sizes, addresses, replicas, options, steps and clipping drawn at
+    random; two steps each."""
+    rng = np.random.default_rng(1000 + seed)
+    pick = lambda *xs: xs[int(rng.integers(len(xs)))]  # noqa: E731
+    p = pick("f32", "bf16", "f16")
+    P = int(rng.integers(1, 12))
+    numels = [int(x) for x in np.exp(rng.uniform(0, math.log(pick(70, 3000, 30000)), P))]
+    numels[int(rng.integers(P))] = pick(0, 1, 64, 256, 1024, 2048, 4096, 8191)
+    betas = pick((0.9, 0.999), (0.0, 0.99), (0.5, 0.0), (0.95, 0.9999))
+    opt = dict(weight_decay=[float(x) for x in rng.uniform(0, 0.2, P)], betas=betas, eps=pick(1e-8, 1e-6, 1e-15),
+               random_seed=int(rng.integers(1 << 62)), step=int(pick(0, 1, 37, 10 ** 6)))
+    if rng.random() < 0.5:
+        opt["lr_scale"] = [float(x) for x in rng.uniform(0, 2, P)]
+    g, state, master = pick("f32", "bf16", "f16"), pick("f32", "f8"), p != "f32" and rng.random() < 0.5
+    R, lead, gap = pick(1, 1, 2, 5), pick(0, 0, 1, 2, 7), pick(0, 0, 1, 3)
+    say(f"random {seed}: p={p} g={g} {state} master={master} R={R} lead={lead} gap={gap} {numels} {opt}")
+    c = Case(p, g, state, master, R=R, lead=lead, gap=gap, numels=numels, seed=seed, **opt)
+    n = D.GradNorm(c.grads) if rng.random() < 0.5 else None
+    for _ in range(2):
+        c.new_grads(scale=pick(1e-4, 1e-2, 1.0))
+        lr, gs = float(10 ** rng.uniform(-5, -1)), float(pick(1.0, 1.0 / 512, -3.0))
+        before = c.host()
+        factor = gs
+        if n is not None:
+            n.compute(max_norm=0.1, grad_scale=gs, skip_nonfinite=True)
+            want = OO.norm(before["g"], gs)
+            assert abs(n.norm.item() - want) <= 2 * OO.U * want
+            factor = gs * n.coef.item()
+        c.opt.step(lr=lr, grad_scale=gs, clip=n)
+        c.check_step(before, lr, factor, f"random {seed}")
 
 
 # ---- norm -------------------------------------------------------------------------------

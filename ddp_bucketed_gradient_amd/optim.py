@@ -83,9 +83,16 @@ class _Handle:
         return self._reducer.h
 
     def close(self):
+        """Release the handle. Work that is still enqueued finishes: no tensor's
+        memory is given to another one before it."""
         if self.h:
             getattr(self.lib, self._destroy)(self.h)
             self.h = None
+            # The caller's tensors may have been allocated for other streams than
+            # the one they are used on; the allocator has to know that one before
+            # the last reference goes. Nothing happens where it is the same.
+            for t in self._keep or ():
+                t.record_stream(self.stream)
             self._keep = None
 
     def __del__(self):
@@ -110,7 +117,7 @@ class GradNorm(_Handle):
 
     def __init__(self, grads: Sequence, stream=None, reducer=None, lib: Optional[_abi.Lib] = None):
         import torch
-        self.h = None
+        self.h = self._keep = None
         lib = lib if lib is not None else _abi.lib()
         grads = list(grads)
         dev = _device(grads, "grads")
@@ -168,7 +175,7 @@ class AdamW(_Handle):
                  lr_scale: Union[None, float, Sequence[float]] = None, states: Optional[dict] = None, step: int = 0,
                  seed: int = 0, stream=None, reducer=None, lib: Optional[_abi.Lib] = None):
         import torch
-        self.h = None
+        self.h = self._keep = None
         lib = lib if lib is not None else _abi.lib()
         params, grads = list(params), list(grads)
         rows = [list(r) for r in params] if params and isinstance(params[0], (list, tuple)) else [params]
@@ -210,7 +217,7 @@ class AdamW(_Handle):
         mp = None if self.master is None else _check(self.master, "master", numel, torch.float32, dev)
         self.lr = lr
         self.params, self.grads = rows, grads
-        self._keep = [rows, grads]
+        self._keep = [t for ts in (*rows, grads, self.master or (), *self._state.values()) for t in ts]
         with torch.cuda.device(dev):
             lib.adamw_bind(h, pp, gp, mp, at["exp_avg"], at["exp_avg_root" if f8 else "exp_avg_sq"],
                            at.get("avg_scale"), at.get("root_scale"), step, self.workspace.data_ptr(),

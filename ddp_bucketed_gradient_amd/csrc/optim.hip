@@ -473,7 +473,8 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, f
 // parameter's update products are fused into the sums they feed. v and r are
 // carried as 2^64 v and 2^32 r, so that no v > 0 is below the normal range that
 // fast_sqrt needs; what then overflows (r > 4e9), or is not finite, takes the
-// way without shortcuts, its whole wave with it.
+// way without shortcuts. Its whole wave goes that way, in which the other
+// elements keep what they have: none depends on what lies beside it.
 template <int PD, int GD, bool MASTER, bool FULL>
 __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, true>& q, const Tile& t, int at,
                                             int lane4, const AdamwArgs& a, const StepValues& s) {
@@ -495,13 +496,14 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
   const v4u random = random_bits(s.hash + static_cast<uint32_t>(at / 4) * kHashIndex, s.key1);
   uint32_t ms, rs, mc, rc;
   if (__builtin_expect(__any(max(mtop, rtop) >= kInf), 0)) {
-    v = decode4(q.rc, q.rs);
-    v = (v * v) * a.beta2 + (g * g) * a.one_minus_beta2;
-    w = widen(q.w);
+    v4f u = decode4(q.rc, q.rs);
+    u = (u * u) * a.beta2 + (g * g) * a.one_minus_beta2;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      r[j] = __builtin_sqrtf(v[j]);
-      w[j] = w[j] * s.decay - (m[j] / (r[j] * s.inv_rbc2 + a.eps)) * s.rate;
+      const bool root = magnitude(r[j]) < kInf;
+      r[j] = root ? r[j] * 0x1p-32f : __builtin_sqrtf(u[j]);
+      if (!root || magnitude(m[j]) >= kInf)
+        w[j] = static_cast<float>(q.w[j]) * s.decay - (m[j] / (r[j] * s.inv_rbc2 + a.eps)) * s.rate;
     }
     mc = encode4_any<false>(m, random, &ms);
     rc = encode4_any<true>(r, random, &rs);

@@ -378,6 +378,9 @@ __device__ __forceinline__ float fast_sqrt(float v) {
   const float r = v * h;
   return __builtin_fmaf(__builtin_fmaf(-r, r, v), 0.5f * h, r);
 }
+// Divisors whose reciprocal is a normal number, too (an estimate of one that is
+// not would be 0 or infinite, and 0 / d then NaN).
+constexpr float kLeastDivisor = 0x1p-126f, kMostDivisor = 0x1p126f;
 __device__ __forceinline__ float fast_div(float x, float d) {
   const float c = __builtin_amdgcn_rcpf(d);
   const float q = x * c;
@@ -395,6 +398,7 @@ struct AdamwArgs {
   double lr, beta1d, beta2d;
   uint64_t seed;
   float grad_scale, beta1, beta2, one_minus_beta1, one_minus_beta2, eps;
+  uint32_t special;      // 8-bit states: waves with an m or r of at least these bits take no shortcuts
   int32_t whole, rests, R, P;
 };
 
@@ -473,8 +477,9 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, f
 // parameter's update products are fused into the sums they feed. v and r are
 // carried as 2^64 v and 2^32 r, so that no v > 0 is below the normal range that
 // fast_sqrt needs; what then overflows (r > 4e9), or is not finite, takes the
-// way without shortcuts. Its whole wave goes that way, in which the other
-// elements keep what they have: none depends on what lies beside it.
+// way without shortcuts, and with an eps outside fast_div's range everything
+// does. A whole wave goes that way, in which the elements that need none of it
+// keep what they have: none depends on what lies beside it.
 template <int PD, int GD, bool MASTER, bool FULL>
 __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, true>& q, const Tile& t, int at,
                                             int lane4, const AdamwArgs& a, const StepValues& s) {
@@ -495,15 +500,16 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
   const uint32_t rtop = max(max(as_bits(r.x), as_bits(r.y)), max(as_bits(r.z), as_bits(r.w)));
   const v4u random = random_bits(s.hash + static_cast<uint32_t>(at / 4) * kHashIndex, s.key1);
   uint32_t ms, rs, mc, rc;
-  if (__builtin_expect(__any(max(mtop, rtop) >= kInf), 0)) {
+  if (__builtin_expect(__any(max(mtop, rtop) >= a.special), 0)) {
     v4f u = decode4(q.rc, q.rs);
     u = (u * u) * a.beta2 + (g * g) * a.one_minus_beta2;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool root = magnitude(r[j]) < kInf;
       r[j] = root ? r[j] * 0x1p-32f : __builtin_sqrtf(u[j]);
-      if (!root || magnitude(m[j]) >= kInf)
-        w[j] = static_cast<float>(q.w[j]) * s.decay - (m[j] / (r[j] * s.inv_rbc2 + a.eps)) * s.rate;
+      const float d = r[j] * s.inv_rbc2 + a.eps;
+      if (!root || magnitude(m[j]) >= kInf || !(d >= kLeastDivisor && d <= kMostDivisor))
+        w[j] = static_cast<float>(q.w[j]) * s.decay - (m[j] / d) * s.rate;
     }
     mc = encode4_any<false>(m, random, &ms);
     rc = encode4_any<true>(r, random, &rs);
@@ -712,6 +718,8 @@ class HipOptimDevice final : public OptimDevice {
     a.one_minus_beta1 = static_cast<float>(1.0 - l.beta1);
     a.one_minus_beta2 = static_cast<float>(1.0 - l.beta2);
     a.eps = static_cast<float>(l.eps);
+    // With eps in range every divisor is: r / sqrt(1 - beta2^t) < 2^32 2^27.
+    a.special = a.eps >= kLeastDivisor && a.eps <= kMostDivisor / 2 ? kInf : 0;
     a.whole = l.whole;
     a.rests = l.rests;
     a.R = l.R;

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import ddp_bucketed_gradient_amd as D  # noqa: F401
-from gpu_util import require_gpu
+from gpu_util import require_gpu, say
 from test_gpu_optim import Case, f64, raw
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +57,32 @@ def test_an_element_does_not_depend_on_the_others(p, master):
     if master:
         x, y = (f64(o.master[0]).reshape(300, 64)[:, other] for o in (a, b))
         assert np.array_equal(x, y)
+
+
+@pytest.mark.parametrize("p,master", [("f32", False), ("bf16", True), ("f16", False)])
+@pytest.mark.parametrize("zero", [True, False])
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 2.0 ** -128, 2.0 ** -126, 2e-38])
+def test_epsilons_around_the_smallest_normal_number(eps, zero, p, master):
+    """0 / (0 + eps) is 0 for every eps > 0, 8-bit states included. In the other
+    elements eps is below 2^-24 of r, so that its own rounding to fp32 (up to a
+    half at 1e-45) does not show."""
+    say(f"eps={eps} zero={zero} p={p}")
+    c = Case(p, "f32", "f8", master, zero=True, seed=81, eps=eps)
+    for _ in range(2):
+        c.new_grads()
+        if zero:
+            for t in c.grads[1::2]:
+                t.zero_()
+            c.grads[10][64:200] = 0.0
+        before = c.host()
+        c.opt.step(lr=1e-2)
+        c.check_step(before, 1e-2, 1.0, f"eps {eps}")
+
+
+@pytest.mark.parametrize("state", ["f32", "f8"])
+def test_epsilon_zero_with_gradients_everywhere(state):
+    c = Case("f32", "f32", state, zero=True, seed=82, eps=0.0)
+    c.new_grads()
+    before = c.host()
+    c.opt.step(lr=1e-2)
+    c.check_step(before, 1e-2, 1.0, "eps 0")

@@ -335,7 +335,8 @@ __device__ __forceinline__ uint32_t encode4(v4f x, uint32_t top, v4u random, uin
   const uint32_t bits = max(top + 0x1FFFFFu, static_cast<uint32_t>(9 + SHIFT) << 23) - (8u << 23);
   *scale = (bits >> 23) - SHIFT;
   const float f = as_float(bits & kInf);
-  const float least = f * 0x1p-9f;       // r = 0: 0 is the middle one; else r 2^127 is over `least` (r < 2^64, > 2^-43)
+  // fmed3: with x = 0, 0 is the middle one; else x 2^127 is over `least` < 2^48 (of all x >= 2^-63, which did not underflow)
+  const float least = f * 0x1p-9f;
   int codes = 0;
 #define DDPB_SR(J)                                                                                     \
   {                                                                                                    \
@@ -369,12 +370,17 @@ __device__ __forceinline__ uint32_t encode4_any(v4f x, v4u random, uint32_t* sca
   return encode4<ROOT, 0>(x, row_max(top4(x)), random, scale) | nan;
 }
 
-// Square root and quotient, correctly rounded for normal arguments whose
-// results are normal (no difference from the IEEE sequences in 16.8 M random
-// arguments each) in 9 and 7 issue slots instead of 16 and 15: an estimate, its
-// residual by fma, one correction. The 8-bit step is bound by instructions.
+// Square root and quotient in 9 and 7 issue slots instead of 16 and 15: an
+// estimate, its residual by fma, one correction. For normal arguments with
+// normal results 16.8 M random ones each gave the bits of the IEEE sequences
+// (samples, no proof). The 8-bit step is bound by instructions.
+//
+// v below 2^-126: the estimate is infinite there (0 and all numbers that are not
+// normal), and its bound of 2^63 = 1 / sqrt(2^-126) takes the root on from 2^-63
+// downwards without a jump: 2^-63 (1.5 c - c^2 / 2) for v = 2^-126 c, never above
+// the true 2^-63 sqrt(c), and 0 for 0.
 __device__ __forceinline__ float fast_sqrt(float v) {
-  const float h = __builtin_fminf(__builtin_amdgcn_rsqf(v), 0x1p64f);   // v = 0: r = 0
+  const float h = __builtin_fminf(__builtin_amdgcn_rsqf(v), 0x1p63f);
   const float r = v * h;
   return __builtin_fmaf(__builtin_fmaf(-r, r, v), 0.5f * h, r);
 }
@@ -475,8 +481,8 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, f
 // 8-bit states. m and v are rounded operation by operation, as in the 32-bit
 // step (one rounding more or less would move a code here and there); in the
 // parameter's update products are fused into the sums they feed. v and r are
-// carried as 2^64 v and 2^32 r, so that no v > 0 is below the normal range that
-// fast_sqrt needs; what then overflows (r > 4e9), or is not finite, takes the
+// carried as 2^64 v and 2^32 r, which keeps v normal for roots down to 2^-95 (below,
+// fast_sqrt lets them underflow gradually); what then overflows (r > 4e9), or is not finite, takes the
 // way without shortcuts, and with an eps outside fast_div's range everything
 // does. A whole wave goes that way, in which the elements that need none of it
 // keep what they have: none depends on what lies beside it.

@@ -445,8 +445,10 @@ int ddpb_norm_compute(ddpb_norm_t n, ddpb_t h, double max_norm, double grad_scal
  *                   rounded stochastically (to nearest, v, which moves by 0.1 %
  *                   a step, would stay on its code), with 16 random bits per
  *                   value from a hash of (seed, t, index): the same bits on
- *                   every run. r > 0 never becomes code 0. An element that is
- *                   not finite becomes NaN. All-zero codes are the zero state. */
+ *                   every run. r > 0 never becomes code 0; below 2^-95 it
+ *                   underflows: it comes out smaller, down to 0. An element
+ *                   that is not finite becomes NaN. All-zero codes are the
+ *                   zero state. */
 typedef struct ddpb_adamw* ddpb_adamw_t;
 
 enum { DDPB_STATE_F32 = 0, DDPB_STATE_F8 = 1 };

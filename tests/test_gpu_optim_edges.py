@@ -9,7 +9,8 @@ import torch
 
 import ddp_bucketed_gradient_amd as D  # noqa: F401
 from gpu_util import require_gpu, say
-from test_gpu_optim import Case, f64, raw
+from oracle import optim as OO
+from test_gpu_optim import Case, check_codes, f64, raw
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +87,42 @@ def test_epsilon_zero_with_gradients_everywhere(state):
     before = c.host()
     c.opt.step(lr=1e-2)
     c.check_step(before, 1e-2, 1.0, "eps 0")
+
+
+def test_roots_around_the_underflow_of_their_squares():
+    """Stored roots from 2^-110 to 2^-85 that decay without a gradient. From
+    2^-95 on (where 2^64 v is a normal number) the new root is within the
+    arithmetic's bound; below, it falls off gradually: never above the true one,
+    at least 0.68 of it down to 2^-96 (the correction step of the root gives
+    1.5 c - c^2 / 2 for c = r^2 2^190 where sqrt(c) is true: 0.6875 of it at c =
+    1/4). Squares there are multiples of 2^-149, two roundings of half a step in
+    c = 2^-23, which 1.5 2^-95 takes to 2^-117.4 in r."""
+    first, last = 17, 42                                    # scales 2^(s - 127), codes from 2^-6 to 448
+    n = 64 * (last - first + 1)
+    c = Case("f32", "f32", "f8", numels=[n], zero=True, seed=83, betas=(0.9, 0.96), step=7, random_seed=5)
+    codes = np.concatenate([np.arange(8, 72) + (s % 2) * 55 for s in range(first, last + 1)]).astype(np.uint8)
+    scales = np.arange(first, last + 1).astype(np.uint8)
+    c.opt.exp_avg_root[0].view(torch.uint8).copy_(torch.from_numpy(codes))
+    c.opt.root_scale[0].view(torch.uint8).copy_(torch.from_numpy(scales))
+    c.grads[0].zero_()
+    r = OO.decode(codes, scales) * math.sqrt(0.96)
+    c.opt.step(lr=1e-2)
+    torch.cuda.synchronize()
+    got_c, got_s = raw(c.opt.exp_avg_root[0]), raw(c.opt.root_scale[0])
+    _, ur = OO.random16(5, 8, np.arange(n, dtype=np.uint64))
+    for b in range(last - first + 1):
+        cut = slice(64 * b, 64 * b + 64)
+        if r[cut].min() >= 2.0 ** -95:
+            check_codes(r[cut], 5 * OO.U * r[cut], ur[cut], True, got_c[cut], got_s[b:b + 1], f"block {b}")
+    s = got_s.astype(np.int64)
+    unit = np.repeat(np.ldexp(1.0, s - 127), 64)
+    got = OO.CODES[got_c]
+    high = r * (1 + 6 * OO.U) + 2.0 ** -117 + unit * 2.0 ** -30
+    low = np.where(r >= 2.0 ** -95, r * (1 - 6 * OO.U), np.where(r >= 2.0 ** -96, 0.68 * r, 0.0)) - unit * 2.0 ** -30
+
+    def at(y):
+        lo, up, pos = OO.encode_levels(np.maximum(y, 0.0), s, ur, True)
+        return np.where(pos >= 1, up, lo)
+    assert (got <= at(high)).all() and (got >= at(low)).all()
+    assert (got[r >= 2.0 ** -96] > 0).all()
+    assert np.array_equal(raw(c.opt.exp_avg[0]) & 127, np.zeros(n, np.uint8))

@@ -273,26 +273,12 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormTile* __re
 // ---------------------------------------------------------------------------
 // AdamW.
 
-// The 16 + 16 random bits of four elements (high half: m, low half: r),
-// counter-based: multiply and xor-shift rounds over the group's index under the
-// step's key, then a short round per element. `h` is the first product plus
-// the first key word, which the caller carries along.
-constexpr uint32_t kHashIndex = 0x9C8E5A6Du, kHashHigh = 0x7F4A3C15u;
-
+// The random bits of a group of four elements.
 __device__ __forceinline__ v4u random_bits(uint32_t h, uint32_t key1) {
-  h ^= h >> 15;
-  h *= 0x85D3B2A7u;
-  h ^= (h >> 13) ^ key1;
-  h *= 0xC5A7E36Bu;
-  h ^= h >> 16;
+  h = hash_mix(h, key1);
   v4u x;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t y = h + j * 0x6D2B4E95u;
-    y ^= y >> 16;
-    y *= 0xB5297A4Du;
-    x[j] = y ^ (y >> 15);
-  }
+  for (int j = 0; j < 4; ++j) x[j] = hash_element(h, j);
   return x;
 }
 
@@ -451,7 +437,8 @@ struct StepValues {      // of the step, in registers
   float gs, inv_rbc2;
   uint32_t key1;
   float decay, rate;     // of the tile's variable
-  uint32_t hash;         // random_bits' h of the lane's first group in the tile
+  uint32_t hash;         // of the lane's first group in the tile
+  uint32_t tile;         // low word of the tile's first group
 };
 
 template <int PD, bool MASTER, bool FULL>
@@ -507,7 +494,7 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
       __builtin_elementwise_maximum(__builtin_fabsf(m.x), __builtin_fabsf(m.y)),
       __builtin_elementwise_maximum(__builtin_fabsf(m.z), __builtin_fabsf(m.w))));    // NaN stays
   const uint32_t rtop = max(max(as_bits(r.x), as_bits(r.y)), max(as_bits(r.z), as_bits(r.w)));
-  const v4u random = random_bits(s.hash + static_cast<uint32_t>(at / 4) * kHashIndex, s.key1);
+  const v4u random = random_bits(hash_at(s.hash, s.tile, threadIdx.x, static_cast<uint32_t>(at / 4)), s.key1);
   uint32_t ms, rs, mc, rc;
   if (__builtin_expect(__any(max(mtop, rtop) >= a.special), 0)) {
     v4f u = decode4(q.rc, q.rs);
@@ -605,10 +592,9 @@ void adamw_kernel(const AdamwArgs a) {
     const double lr = a.lr_device != nullptr ? static_cast<double>(constant(a.lr_device)) : a.lr;
     s.decay = static_cast<float>(1.0 - lr * x.lr_scale * x.weight_decay);
     s.rate = static_cast<float>(lr * x.lr_scale * sc.inv_bc1);
-    // Tiles start on multiples of 64, so none crosses a multiple of 2^32 groups.
     const uint64_t group = x.group0 + from / 4;
-    s.hash = (static_cast<uint32_t>(group) + threadIdx.x) * kHashIndex +
-             static_cast<uint32_t>(group >> 32) * kHashHigh + sc.key0;
+    s.hash = hash_start(group, threadIdx.x, sc.key0);
+    s.tile = static_cast<uint32_t>(group);
     return s;
   };
   if (at + S::kPart <= t.len) {

@@ -131,6 +131,40 @@ DDPB_HD inline StepScalars step_scalars(int64_t done, double beta1, double beta2
   return s;
 }
 
+// The 16 + 16 random bits of an element (high half: m, low half: r),
+// counter-based: multiply and xor-shift rounds over the 64-bit index of its
+// group of four elements under the step's key, then a short round for each
+// element. A lane starts from the hash of its first group in a tile and goes on
+// by `groups`, which are few; the index's high word changes where the low one
+// wraps, inside one tile in 4 G groups at most.
+constexpr uint32_t kHashIndex = 0x9C8E5A6Du, kHashHigh = 0x7F4A3C15u;
+
+// The hash of group `tile` + `lane`, but for a wrap between the two.
+DDPB_HD inline uint32_t hash_start(uint64_t tile, uint32_t lane, uint32_t key0) {
+  return (static_cast<uint32_t>(tile) + lane) * kHashIndex + static_cast<uint32_t>(tile >> 32) * kHashHigh + key0;
+}
+// The hash of group `tile` + `lane` + `groups` from that start; `tile_low` is
+// the low word of the tile's first group.
+DDPB_HD inline uint32_t hash_at(uint32_t start, uint32_t tile_low, uint32_t lane, uint32_t groups) {
+  uint32_t h = start + groups * kHashIndex;
+  if (__builtin_expect(tile_low > UINT32_MAX - static_cast<uint32_t>(kOptimTile / 4 - 1), 0))
+    h += tile_low + lane + groups < tile_low ? kHashHigh : 0;
+  return h;
+}
+DDPB_HD inline uint32_t hash_mix(uint32_t h, uint32_t key1) {
+  h ^= h >> 15;
+  h *= 0x85D3B2A7u;
+  h ^= (h >> 13) ^ key1;
+  h *= 0xC5A7E36Bu;
+  return h ^ (h >> 16);
+}
+DDPB_HD inline uint32_t hash_element(uint32_t mixed, uint32_t j) {
+  uint32_t y = mixed + j * 0x6D2B4E95u;
+  y ^= y >> 16;
+  y *= 0xB5297A4Du;
+  return y ^ (y >> 15);
+}
+
 struct NormLaunch {
   void* stream;
   int device;

@@ -480,8 +480,8 @@ int ddpb_adamw_workspace_bytes(ddpb_adamw_t a, int64_t* bytes);
  * Every array contiguous and aligned to its element type (NULL where numel is
  * 0). The memory that a step writes must not overlap anything else named here:
  * DDPB_E_ARG for a tied parameter listed twice, and for more workgroups than
- * one launch takes (17 G elements). Uploads the tables and synchronizes the
- * stream once. */
+ * one launch takes (17 G elements; 34 G with 8-bit states and 16-bit parameters
+ * without masters). Uploads the tables and synchronizes the stream once. */
 int ddpb_adamw_bind(ddpb_adamw_t a, void* const* params, void* const* grads, void* const* master,
                     void* const* exp_avg, void* const* second, void* const* avg_scale, void* const* root_scale,
                     int64_t step, void* workspace, int64_t ws_bytes, void* stream, ddpb_t h);

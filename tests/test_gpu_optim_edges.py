@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-import ddp_bucketed_gradient_amd as D  # noqa: F401
+import ddp_bucketed_gradient_amd as D
 from gpu_util import require_gpu, say
 from oracle import optim as OO
 from test_gpu_optim import Case, check_codes, f64, raw
@@ -126,3 +126,38 @@ def test_roots_around_the_underflow_of_their_squares():
     assert (got <= at(high)).all() and (got >= at(low)).all()
     assert (got[r >= 2.0 ** -96] > 0).all()
     assert np.array_equal(raw(c.opt.exp_avg[0]) & 127, np.zeros(n, np.uint8))
+
+
+def test_random_bits_where_a_tile_crosses_2_to_the_32_groups():
+    """A second variable whose groups of four elements pass index 2^32 inside a
+    tile: in its first wave, in the second group of a lane, and in a rest."""
+    big, n1 = 1 << 34, 4096 + 1500
+    need = (big + n1) * 6 + (8 << 30)
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+    new = lambda n, dt: torch.zeros(n, dtype=torch.uint8, device="cuda").view(dt)  # noqa: E731
+    p0, g0 = new(2 * big, torch.bfloat16), new(2 * big, torch.bfloat16)
+    m0, r0 = new(big, torch.float8_e4m3fn), new(big, torch.float8_e4m3fn)
+    ms0, rs0 = new(big // 64, torch.float8_e8m0fnu), new(big // 64, torch.float8_e8m0fnu)
+    gen = torch.Generator(device="cuda").manual_seed(86)
+    for cross in (64, 2048 + 1088, 4096 + 1088):            # elements of variable 1 below 2^34
+        say(f"2^32 groups reached at element {cross}")
+        n0 = big - cross
+        p = (torch.randn(n1, generator=gen, device="cuda") * 0.02).bfloat16()
+        g = (torch.randn(n1, generator=gen, device="cuda") * 1e-3).bfloat16()
+        opt = D.AdamW([p0[:n0], p], [g0[:n0], g], lr=1e-2, weight_decay=0.0, state="f8", seed=99, states={
+            "exp_avg": [m0[:n0], new(n1, torch.float8_e4m3fn)], "exp_avg_root": [r0[:n0], new(n1, torch.float8_e4m3fn)],
+            "avg_scale": [ms0[:-(-n0 // 64)], new(-(-n1 // 64), torch.float8_e8m0fnu)],
+            "root_scale": [rs0[:-(-n0 // 64)], new(-(-n1 // 64), torch.float8_e8m0fnu)]})
+        w0, gg = f64(p), f64(g)
+        opt.step()
+        torch.cuda.synchronize()
+        (_, m, _, r), (_, bm, _, br) = OO.adamw(w0, gg, 0 * gg, 0 * gg, t=1, lr=1e-2, beta1=0.9, beta2=0.999, eps=1e-8,
+                                                weight_decay=0.0, gscale=1.0)
+        um, ur = OO.random16(99, 1, np.uint64(n0) + np.arange(n1, dtype=np.uint64))
+        check_codes(m, bm, um, False, raw(opt.exp_avg[1]), raw(opt.avg_scale[1]), f"m, crossing at {cross}")
+        check_codes(r, br, ur, True, raw(opt.exp_avg_root[1]), raw(opt.root_scale[1]), f"r, crossing at {cross}")
+        opt.close()
+        del opt
+    del p0, g0, m0, r0, ms0, rs0
+    torch.cuda.empty_cache()

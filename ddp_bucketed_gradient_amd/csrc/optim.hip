@@ -264,9 +264,10 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormTile* __re
   acc = block_sum(acc, lds);
   if (threadIdx.x == 0) {
     const double n = __builtin_sqrt(acc) * __builtin_fabs(grad_scale);
-    result->norm = static_cast<float>(n);
+    const float norm = static_cast<float>(n);   // infinite above fp32's range
+    result->norm = norm;
     result->coef = n > max_norm ? static_cast<float>(max_norm / n) : 1.0f;
-    result->skip = skip_nonfinite && !__builtin_isfinite(n);
+    result->skip = skip_nonfinite && !__builtin_isfinite(norm);
   }
 }
 

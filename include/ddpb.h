@@ -404,7 +404,7 @@ typedef struct ddpb_norm* ddpb_norm_t;
 struct ddpb_norm_result {
   float norm;
   float coef;
-  int32_t skip;       /* 1: the norm was not finite and DDPB_NORM_SKIP_NONFINITE was set */
+  int32_t skip;       /* 1: `norm` is not finite (in fp32) and DDPB_NORM_SKIP_NONFINITE was set */
   uint32_t reserved;
 };
 

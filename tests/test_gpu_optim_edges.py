@@ -161,3 +161,24 @@ def test_random_bits_where_a_tile_crosses_2_to_the_32_groups():
         del opt
     del p0, g0, m0, r0, ms0, rs0
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("state", ["f32", "f8"])
+def test_a_norm_above_the_range_of_fp32_is_not_finite(state):
+    """Finite gradients whose norm fp32 cannot hold: the norm that is reported is
+    infinite, and a step that is to be skipped on such a norm is."""
+    c = Case("f32", "f32", state, seed=85)
+    c.new_grads()
+    c.grads[9].fill_(3e38)
+    n = D.GradNorm(c.grads)
+    before = {k: s.bytes.cpu().numpy() for k, s in c.stores.items()}
+    norm = n.compute(max_norm=1.0, skip_nonfinite=True)
+    c.opt.step(lr=1e-2, clip=n)
+    torch.cuda.synchronize()
+    assert math.isinf(norm.item()) and n.skipped.item() == 1 and c.opt.steps_done == 0
+    for k, s in c.stores.items():
+        assert np.array_equal(before[k], s.bytes.cpu().numpy()), k
+    n.compute(max_norm=1.0, grad_scale=2.0 ** -20, skip_nonfinite=True)      # in range again
+    assert math.isfinite(norm.item()) and n.skipped.item() == 0
+    n.compute(max_norm=1.0)                                                  # nobody asked to skip
+    assert math.isinf(norm.item()) and n.skipped.item() == 0

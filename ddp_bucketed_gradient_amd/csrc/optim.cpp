@@ -303,8 +303,8 @@ int Adamw::step(const Reducer* red, double lr, const float* lr_device, double gr
     *err = "adamw step: not bound";
     return kErrState;
   }
-  if (!std::isfinite(lr) || lr < 0 || !std::isfinite(grad_scale)) {
-    *err = "adamw step: lr must be finite and not negative, grad_scale finite";
+  if (!std::isfinite(lr) || lr < 0 || !std::isfinite(static_cast<float>(grad_scale))) {
+    *err = "adamw step: lr must be finite and not negative, grad_scale finite in fp32";
     return kErrArg;
   }
   if (!aligned(lr_device, 4) || !aligned(clip, 4)) {

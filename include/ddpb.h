@@ -489,6 +489,7 @@ int ddpb_adamw_bind(ddpb_adamw_t a, void* const* params, void* const* grads, voi
 /*   lr, lr_device  the rate: a host value (finite, >= 0), or, if not NULL, the
  *                  fp32 at that device address when the step runs (so that a
  *                  replayed graph follows a schedule)
+ *   grad_scale     finite in fp32
  *   clip           NULL, or the workspace of a bound norm whose compute was
  *                  enqueued before on the same stream: g' takes its coef, and
  *                  with its skip set the step changes nothing and does not count */

@@ -182,3 +182,17 @@ def test_a_norm_above_the_range_of_fp32_is_not_finite(state):
     assert math.isfinite(norm.item()) and n.skipped.item() == 0
     n.compute(max_norm=1.0)                                                  # nobody asked to skip
     assert math.isinf(norm.item()) and n.skipped.item() == 0
+
+
+@pytest.mark.parametrize("state", ["f32", "f8"])
+def test_gradients_that_are_not_finite_leave_nan(state):
+    """An infinite gradient makes m and r infinite, their quotient is NaN; NaN
+    stays NaN. Every other parameter is finite."""
+    c = Case("f32", "f32", state, zero=True, seed=84)
+    c.new_grads()
+    bad = np.zeros(12345, dtype=bool)
+    for i, x in {0: math.inf, 63: -math.inf, 64: math.nan, 4500: math.inf, 12344: math.nan}.items():
+        c.grads[9][i] = x
+        bad[i] = True
+    c.opt.step(lr=1e-3)
+    assert np.array_equal(np.isnan(f64(c.opt.params[0][9])), bad)

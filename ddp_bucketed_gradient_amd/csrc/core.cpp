@@ -48,6 +48,7 @@ int Reducer::bind(const BindArgs& args, std::string* err) {
   }
   bound_ = (rc == kOk);
   bind_id_ = ++g_binds;
+  averaged_ = true;
   static_bind_ = bound_ && args.no_alloc;
   sync_step_set_ = false;          // the launcher's tables were released
   // The launch log and the timing history refer to the previous binding's
@@ -77,6 +78,14 @@ int Reducer::check_idle(const char* what, std::string* err) const {
     *err = std::string(what) + ": an iteration is in progress; the gradients are final after ddpb_finalize";
     return kErrState;
   }
+  if (sync_step_set_) {
+    *err = std::string(what) + ": a step is set for the coming synchronisation (ddpb_set_sync_step)";
+    return kErrState;
+  }
+  if (!averaged_) {
+    *err = std::string(what) + ": the gradients were written since the last synchronisation and are not averaged";
+    return kErrState;
+  }
   return kOk;
 }
 
@@ -89,7 +98,10 @@ int Reducer::mark_ready(int32_t v, std::string* err) {
     *err = "mark_ready: variable index out of range";
     return kErrIndex;
   }
-  if (!sync_) return kOk;     // no_sync: the hook runs but does nothing
+  if (!sync_) {               // no_sync: the hook runs but reduces nothing
+    averaged_ = false;
+    return kOk;
+  }
   if (failed_) {
     *err = "the previous iteration left buckets unreduced; a new iteration cannot start before ddpb_reset";
     return kErrIncomplete;
@@ -98,6 +110,7 @@ int Reducer::mark_ready(int32_t v, std::string* err) {
     // [C30] "Unused Parameter": once per iteration, at its first hook (even if
     // that hook then fails), the unused variables are marked ready.
     started_ = true;
+    averaged_ = false;
     log_.clear();
     const int rc = mark_unused_ready(calls_, err);
     if (rc != kOk) {
@@ -216,6 +229,7 @@ int Reducer::finalize(std::string* err) {
   if (!sync_ && !started_) return kOk;
   if (!failed_ && !started_) {            // no hook fired: only unused variables, if any
     started_ = true;
+    averaged_ = false;
     log_.clear();
     const int rc = mark_unused_ready(0, err);
     if (rc != kOk) {
@@ -237,6 +251,7 @@ int Reducer::finalize(std::string* err) {
   // [C30] "Finalize Backward 与梯度可见性": the compute stream is ordered after
   // every bucket's reduction, without a host synchronization.
   const int rc = launcher_->join(err);
+  averaged_ = (rc == kOk);
   log_ring_[finalized_ % kTimeRing] = log_;
   // a rebuild needs every variable's place in the ready order ([C30]: no
   // ready-order rebuild when the set of used parameters changes)
@@ -289,6 +304,7 @@ int Reducer::accumulate(void* const* step_ptrs, int32_t step_dtype, bool first, 
     *err = "no_sync_accumulate: an iteration is in progress (finalize it first)";
     return kErrState;
   }
+  averaged_ = false;
   return launcher_->accumulate(step_ptrs, step_dtype, first, err);
 }
 

@@ -189,7 +189,8 @@ class Reducer {
   // AdamW) took its gradient addresses from one binding.
   int64_t bind_id() const { return bound_ ? bind_id_ : 0; }
   // kErrState while an iteration is open (its buckets may still be reducing),
-  // kErrIncomplete while a failed one is latched.
+  // a step is set for the coming synchronisation, or the gradients have been
+  // written since the last one; kErrIncomplete while a failed one is latched.
   int check_idle(const char* what, std::string* err) const;
 
  private:
@@ -202,6 +203,9 @@ class Reducer {
   int64_t bind_id_ = 0;
   bool static_bind_ = false;       // bound by ddpb_bind_static: no staging for tables
   bool sync_ = true;
+  // As far as this handle can know: no local step, hook without synchronisation
+  // or unfinished iteration since the last synchronisation (or the bind).
+  bool averaged_ = true;
   bool failed_ = false;            // latched "prior reduction did not finish"
   std::vector<int32_t> pending_;   // per bucket
   std::vector<uint8_t> ready_;     // per variable

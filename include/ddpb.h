@@ -388,11 +388,14 @@ int ddpb_reset(ddpb_t h);
  *
  * The ddpb_t argument (bind, compute, step) may be NULL. With a reducer, bind
  * notes the reducer's present binding (DDPB_E_STATE if it is unbound), and
- * compute and step refuse while an iteration is open or the reducer has been
- * bound again since (DDPB_E_STATE) or a failed iteration is latched
- * (DDPB_E_INCOMPLETE): the gradients are not the averaged ones then. Pass the
- * gradient addresses of one replica (they are equal on all) and the reducer's
- * compute stream.
+ * compute and step refuse where the gradients are not the averaged ones: while
+ * an iteration is open, once the reducer has been bound again, with a step set
+ * for the coming synchronisation, and after ddpb_no_sync_accumulate, a hook
+ * with synchronisation off or an iteration that was reset, until the next
+ * synchronisation (DDPB_E_STATE), or while a failed iteration is latched
+ * (DDPB_E_INCOMPLETE). Gradients that the caller wrote without telling the
+ * reducer are not noticed. Pass the gradient addresses of one replica (they are
+ * equal on all) and the reducer's compute stream.
  */
 
 /* Global norm of P tensors: norm = |grad_scale| * sqrt(sum of all squares),

@@ -193,10 +193,13 @@ class AdamW(_Handle):
         pp = [a for r, row in enumerate(rows) for a in _check(row, f"params[{r}]", numel, pt, dev)]
         gp = _check(grads, "grads", numel, gt, dev)
         every = lambda x: [float(x)] * P if isinstance(x, _Real) else [float(y) for y in x]  # noqa: E731
+        self._options = {"betas": (float(betas[0]), float(betas[1])), "eps": float(eps),
+                         "weight_decay": every(weight_decay), "lr_scale": None if lr_scale is None else every(lr_scale),
+                         "state": state, "seed": int(seed)}
         h = lib.adamw_create(numel, len(rows), pc, gc, _abi.STATE_F8 if f8 else _abi.STATE_F32,
                              _abi.ADAMW_MASTER if master is not None and master is not False else 0,
-                             float(betas[0]), float(betas[1]), float(eps), every(weight_decay),
-                             None if lr_scale is None else every(lr_scale), seed)
+                             *self._options["betas"], self._options["eps"], self._options["weight_decay"],
+                             self._options["lr_scale"], seed)
         self._open(lib, h, dev, stream, reducer)
         with torch.cuda.device(dev), torch.cuda.stream(self.stream):
             self.master = None
@@ -263,10 +266,21 @@ class AdamW(_Handle):
 
     @property
     def states(self) -> dict:
-        """The state's tensors, as the argument ``states`` takes them: to save,
-        or to go on with in a new AdamW (with ``step=old.steps_done``) when
-        gradients or parameters have moved. It continues bit for bit."""
+        """The state's tensors, as the argument ``states`` takes them."""
         return {k: list(v) for k, v in self._state.items()}
+
+    @property
+    def options(self) -> dict:
+        """Every argument but the tensors to update and the count of steps:
+        rate, betas, eps, weight decay, rate factors, state type and seed, with
+        the state and the masters as they stand. A new AdamW on the same
+        parameters, or on copies after a restart or with gradients that have
+        moved, goes on bit for bit when it is made with
+        ``step=old.steps_done, **old.options``. (The tensors are shared, not
+        copied: wait for the stream before saving them, and leave the old handle
+        alone afterwards.)"""
+        return {**self._options, "lr": self.lr, "states": self.states,
+                "master": None if self.master is None else list(self.master)}
 
     @property
     def steps_done(self) -> int:

@@ -1,11 +1,13 @@
 """What a program around the AdamW step relies on: tensors let go while a step is
-in flight.
+in flight, and a handle made again from another's options.
 """
+import numpy as np
 import pytest
 import torch
 
 import ddp_bucketed_gradient_amd as D
 from gpu_util import require_gpu
+from test_gpu_optim import Case, raw
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +45,25 @@ def test_memory_let_go_behind_a_step_is_not_reused_before_it(state):
           [torch.full((k,), 7, dtype=torch.uint8, device="cuda") for k in (n, n, n // 64, n // 64)]
     torch.cuda.synchronize()
     assert all((t == 7).all().item() for t in new)
+
+
+@pytest.mark.parametrize("p,state,master", [("bf16", "f8", True), ("f32", "f8", False), ("f16", "f32", True)])
+def test_options_make_a_handle_that_goes_on_bit_for_bit(p, state, master):
+    """Another seed than 0, other betas, eps, decay and rate factors than the
+    defaults: a handle made from ``options`` draws the same bits and takes the
+    same steps."""
+    n = len(Case(zero=True).numels)
+    a, b = (Case(p, "f32", state, master, seed=91, step=9, random_seed=1234, betas=(0.8, 0.97), eps=1e-6, lr=3e-2,
+                 weight_decay=[0.01 * v for v in range(n)], lr_scale=[1 + 0.1 * v for v in range(n)]) for _ in range(2))
+    for rep in range(4):
+        for c in (a, b):
+            c.new_grads()
+            c.opt.step()
+        old = b.opt
+        b.opt = D.AdamW(old.params[0], old.grads, step=old.steps_done, **old.options)
+        assert b.opt.lr == 3e-2
+        old.close()
+    torch.cuda.synchronize()
+    assert a.opt.steps_done == b.opt.steps_done == 13
+    for k in a.stores:
+        assert np.array_equal(a.stores[k].bytes.cpu().numpy(), b.stores[k].bytes.cpu().numpy()), k

@@ -220,6 +220,10 @@ class AdamW(_Handle):
         mp = None if self.master is None else _check(self.master, "master", numel, torch.float32, dev)
         self.lr = lr
         self.params, self.grads = rows, grads
+        # The step writes through addresses; autograd counts writes by tensor, to
+        # refuse a backward that needs the values from before.
+        self._count_write = torch.autograd.graph.increment_version
+        self._written = [t for row in (*rows, self.master or ()) for t in row]
         self._keep = [t for ts in (*rows, grads, self.master or (), *self._state.values()) for t in ts]
         with torch.cuda.device(dev):
             lib.adamw_bind(h, pp, gp, mp, at["exp_avg"], at["exp_avg_root" if f8 else "exp_avg_sq"],
@@ -249,7 +253,9 @@ class AdamW(_Handle):
     def step(self, lr=None, grad_scale: float = 1.0, clip: Optional[GradNorm] = None):
         """Enqueue one step. ``lr`` (default: the attribute) and ``grad_scale``
         (the factor that takes a loss scale out) as in the class; ``clip``: a
-        GradNorm on the same stream whose compute() was called before."""
+        GradNorm on the same stream whose compute() was called before.
+        Parameters and masters count as written in place for autograd, by the
+        call; replays of a graph that captured it are not seen."""
         lr = self.lr if lr is None else lr
         at = 0
         if type(lr) is not float and not isinstance(lr, _Real):
@@ -263,6 +269,7 @@ class AdamW(_Handle):
                 raise ValueError("clip must run on the same stream as the step")
             result = clip._result
         self.lib.adamw_step(self.h, lr, at, grad_scale, result, self._red())
+        self._count_write(self._written)
 
     @property
     def states(self) -> dict:

@@ -1,5 +1,5 @@
 """What a program around the AdamW step relies on: tensors let go while a step is
-in flight, and a handle made again from another's options.
+in flight, a handle made again from another's options, autograd's in-place check.
 """
 import numpy as np
 import pytest
@@ -67,3 +67,21 @@ def test_options_make_a_handle_that_goes_on_bit_for_bit(p, state, master):
     assert a.opt.steps_done == b.opt.steps_done == 13
     for k in a.stores:
         assert np.array_equal(a.stores[k].bytes.cpu().numpy(), b.stores[k].bytes.cpu().numpy()), k
+
+
+def test_autograd_sees_the_step():
+    """A backward that saved the old parameters is refused, as after an in-place
+    operation of torch's own; every replica counts."""
+    rows = [[torch.nn.Parameter(torch.ones(10, device="cuda"))] for _ in range(2)]
+    opt = D.AdamW(rows, [torch.ones(10, device="cuda")])
+    before = [r[0]._version for r in rows]
+    losses = [(r[0] * r[0]).sum() for r in rows]
+    opt.step()
+    for r, b, loss in zip(rows, before, losses):
+        assert r[0]._version > b
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+    with torch.inference_mode():
+        x = torch.ones(3, device="cuda")                  # has no counter
+    D.AdamW([x], [torch.ones(3, device="cuda")], lr=0.125, weight_decay=0.0).step()
+    assert (x < 1).all().item()

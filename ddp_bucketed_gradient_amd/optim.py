@@ -166,7 +166,8 @@ class AdamW(_Handle):
     Attributes: ``exp_avg`` and ``exp_avg_sq`` (fp32) or ``exp_avg``,
     ``exp_avg_root`` (float8_e4m3fn), ``avg_scale``, ``root_scale``
     (float8_e8m0fnu); ``master``; ``lr`` (a float, or a 1-element fp32 CUDA
-    tensor that the step reads when it runs).
+    tensor that the step reads when it runs, behind what the current stream has
+    enqueued; it has to live as long as a graph that captured the step).
     """
     _destroy = "adamw_destroy"
 
@@ -262,6 +263,12 @@ class AdamW(_Handle):
             import torch
             if not isinstance(lr, torch.Tensor) or lr.dtype != torch.float32 or not lr.is_cuda or lr.device != self.device or lr.numel() != 1:
                 raise ValueError("lr must be a number or a 1-element fp32 CUDA tensor on the parameters' device")
+            # read when the step runs, behind what the current stream wrote; in a
+            # capture the caller has ordered the streams (or they are the same)
+            now = torch.cuda.current_stream(self.device)
+            if now != self.stream and not torch.cuda.is_current_stream_capturing():
+                self.stream.wait_stream(now)
+            lr.record_stream(self.stream)
             at, lr = lr.data_ptr(), 0.0
         result = 0
         if clip is not None:

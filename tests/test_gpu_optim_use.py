@@ -1,5 +1,6 @@
 """What a program around the AdamW step relies on: tensors let go while a step is
-in flight, a handle made again from another's options, autograd's in-place check.
+in flight, a handle made again from another's options, autograd's in-place check,
+a rate in device memory.
 """
 import numpy as np
 import pytest
@@ -85,3 +86,28 @@ def test_autograd_sees_the_step():
         x = torch.ones(3, device="cuda")                  # has no counter
     D.AdamW([x], [torch.ones(3, device="cuda")], lr=0.125, weight_decay=0.0).step()
     assert (x < 1).all().item()
+
+
+def test_a_rate_written_on_another_stream():
+    """A rate that the busy current stream writes, a step on a side stream, the
+    rate let go and its memory written again at once: the step takes the value
+    that was written before it."""
+    side = torch.cuda.Stream()
+    a, b = (Case("f32", "f32", "f32", seed=93, stream=s) for s in (side, None))
+    for c in (a, b):
+        c.new_grads()
+    x = torch.randn(4096, 4096, device="cuda")
+    lr = torch.full((1,), 0.5, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        x = x @ x * 1e-3                                  # keeps the current stream busy
+    lr.fill_(0.125)
+    a.opt.step(lr=lr)
+    del lr
+    new = [torch.full((1,), 7.0, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    b.opt.step(lr=0.125)
+    torch.cuda.synchronize()
+    for k in a.stores:
+        assert np.array_equal(a.stores[k].bytes.cpu().numpy(), b.stores[k].bytes.cpu().numpy()), k
+    assert all(t.item() == 7.0 for t in new)

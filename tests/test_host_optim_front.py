@@ -1,5 +1,8 @@
 """The norm's and AdamW's Python front end on the CPU, with stand-ins for
 tensors and streams where a GPU would be needed."""
+import pytest
+import torch
+
 import ddp_bucketed_gradient_amd as D
 
 
@@ -37,3 +40,37 @@ def test_tensors_let_go_by_close_are_known_on_the_stream_that_uses_them():
             assert all(t.streams == [x.stream] for t in ts)
             x.close()                                    # once only
             assert all(len(t.streams) == 1 for t in ts) and len(x.lib.calls) == 1
+
+
+class FakeStream:
+    def __init__(self):
+        self.waited = []
+
+    def wait_stream(self, s):
+        self.waited.append(s)
+
+
+class FakeRate(torch.Tensor):
+    is_cuda, device = True, "gpu"
+
+    def record_stream(self, s):
+        self.__dict__.setdefault("streams", []).append(s)
+
+
+@pytest.mark.parametrize("elsewhere,capturing", [(False, False), (True, False), (True, True), (False, True)])
+def test_a_rate_in_device_memory_is_read_behind_what_wrote_it(monkeypatch, elsewhere, capturing):
+    """The step reads it on the handle's stream: behind what the current one has
+    enqueued so far, and its memory stays. In a capture the caller has ordered
+    the two streams (a wait would draw the handle's stream into the capture)."""
+    own, other = FakeStream(), FakeStream()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: other if elsewhere else own)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    x = _handle(D.AdamW, device="gpu", _state={}, _written=[], _count_write=lambda ts: None)
+    x.stream = own
+    lr = torch.ones(1).as_subclass(FakeRate)
+    x.step(lr=lr)
+    assert x.lib.calls[-1][0] == "adamw_step" and x.lib.calls[-1][1][2] == lr.data_ptr()
+    assert own.waited == ([other] if elsewhere and not capturing else [])
+    assert lr.streams == [own]
+    x.step(lr=1e-3)                                      # a number needs neither
+    assert own.waited == ([other] if elsewhere and not capturing else []) and lr.streams == [own]

@@ -61,6 +61,8 @@ class _Handle:
         import torch
         self.lib, self.h, self.device, self._reducer = lib, h, device, reducer
         if reducer is not None:
+            if getattr(reducer, "compute_stream", None) is None:
+                raise _abi.DdpbError(_abi.E_STATE, "the reducer is not bound to tensors")
             if stream is not None and stream != reducer.compute_stream:
                 raise ValueError("with a reducer the stream is its compute stream")
             stream = reducer.compute_stream

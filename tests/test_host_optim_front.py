@@ -1,5 +1,7 @@
 """The norm's and AdamW's Python front end on the CPU, with stand-ins for
 tensors and streams where a GPU would be needed."""
+import os
+
 import pytest
 import torch
 
@@ -74,3 +76,18 @@ def test_a_rate_in_device_memory_is_read_behind_what_wrote_it(monkeypatch, elsew
     assert lr.streams == [own]
     x.step(lr=1e-3)                                      # a number needs neither
     assert own.waited == ([other] if elsewhere and not capturing else []) and lr.streams == [own]
+
+
+def test_a_reducer_without_a_stream_is_refused():
+    """Unbound, or bound to raw addresses only: no stream to run on is known."""
+    if not os.path.exists(D.HOSTONLY_LIB):
+        from ddp_bucketed_gradient_amd import build
+        build.build_hostonly()
+    red = D.Reducer([(10,)], 2, 0, lib=D.Lib(D.HOSTONLY_LIB))
+    for bind in (lambda: None, lambda: red.bind_ptrs([0x1000, 0x2000])):
+        bind()
+        x = _handle(D.GradNorm)
+        with pytest.raises(D.DdpbError) as e:
+            x._open(x.lib, x.h, torch.device("cuda", 0), None, red)
+        assert e.value.code == D.E_STATE
+    red.close()

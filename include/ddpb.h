@@ -451,7 +451,12 @@ int ddpb_norm_compute(ddpb_norm_t n, ddpb_t h, double max_norm, double grad_scal
  *                   every run. r > 0 never becomes code 0; below 2^-95 it
  *                   underflows: it comes out smaller, down to 0. An element
  *                   that is not finite becomes NaN. All-zero codes are the
- *                   zero state. */
+ *                   zero state. The rounding is unbiased in r; r^2, which the
+ *                   next step takes for v, gains its variance: in the long run
+ *                   it lies above v by q / (2 r) E|g^2 / v - 1|, q the distance
+ *                   between codes at r. With normal gradients that is 3-6 %
+ *                   (steps 1.5-3 % shorter) for elements down to 1e-4 of their
+ *                   block's largest, whatever beta2, and a half at 1e-5. */
 typedef struct ddpb_adamw* ddpb_adamw_t;
 
 enum { DDPB_STATE_F32 = 0, DDPB_STATE_F8 = 1 };

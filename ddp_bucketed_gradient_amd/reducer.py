@@ -272,7 +272,9 @@ class Reducer:
     def adamw(self, params, **options) -> "AdamW":
         """AdamW on the averaged gradients: ``params`` R x P (every replica's
         parameters receive the step) or P tensors; ``options`` as for AdamW.
-        Steps run on the compute stream, behind finalize; made once per binding."""
+        Steps run on the compute stream, behind finalize; made once per binding.
+        A variable that no replica used takes the step with the gradient that
+        stands there (as it was before the sync; zeros with bucket views)."""
         return AdamW(params, self._replica_grads(), reducer=self, lib=self.lib, **options)
 
     # -- diagnostics -------------------------------------------------------------------

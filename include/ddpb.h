@@ -395,7 +395,14 @@ int ddpb_reset(ddpb_t h);
  * synchronisation (DDPB_E_STATE), or while a failed iteration is latched
  * (DDPB_E_INCOMPLETE). Gradients that the caller wrote without telling the
  * reducer are not noticed. Pass the gradient addresses of one replica (they are
- * equal on all) and the reducer's compute stream.
+ * equal on all, but for the next case) and the reducer's compute stream.
+ *
+ * A variable that no replica used (ddpb_set_local_used) is part of the norm and
+ * of the step like any other, with the gradient that stands at its address: in
+ * copy modes the one from before (each replica its own, replica 0's is taken),
+ * with bucket views zeros. Its states decay and weight decay applies. Zero such
+ * gradients, or give variables that may stay unused handles of their own and
+ * leave out their step.
  */
 
 /* Global norm of P tensors: norm = |grad_scale| * sqrt(sum of all squares),

@@ -1,6 +1,6 @@
 """What a program around the AdamW step relies on: tensors let go while a step is
 in flight, a handle made again from another's options, autograd's in-place check,
-a rate in device memory.
+a rate in device memory, variables that were not used.
 """
 import numpy as np
 import pytest
@@ -111,3 +111,29 @@ def test_a_rate_written_on_another_stream():
     for k in a.stores:
         assert np.array_equal(a.stores[k].bytes.cpu().numpy(), b.stores[k].bytes.cpu().numpy()), k
     assert all(t.item() == 7.0 for t in new)
+
+
+@pytest.mark.parametrize("view", [False, True])
+def test_a_variable_that_no_replica_used_takes_the_step_as_it_stands(view):
+    """Its gradient is what was there before the synchronisation (replica 0's),
+    or zeros with bucket views."""
+    shapes, R = [(100,), (70,), (300,)], 2
+    red = D.Reducer(shapes, R, 4 * 200)
+    grads = red.bind_bucket_views() if view else [[torch.empty(s, device="cuda") for s in shapes] for _ in range(R)]
+    if not view:
+        red.bind(grads)
+    for r in range(R):
+        for v, t in enumerate(grads[r]):
+            t.fill_(1.0 + r + v)
+    params = [torch.ones(s, device="cuda") for s in shapes]
+    opt = red.adamw(params, lr=0.25, weight_decay=0.5, betas=(0.0, 0.0), eps=0.125)
+    red.set_local_used([[True, False, True]] * R)
+    red.sync([2, 0])
+    opt.step()
+    torch.cuda.synchronize()
+    # with both betas 0: p (1 - lr wd) - lr g / (|g| + eps)
+    for p, g in zip(params, (1.5, 0.0 if view else 2.0, 3.5)):
+        want = 0.875 - 0.25 * g / (g + 0.125)
+        # p's factor, product and difference (3 roundings of at most 1) and 13 of an update below lr
+        assert (p.double() - want).abs().max().item() <= 2.0 ** -24 * (3 + 13 * 0.25)
+    red.close()

@@ -172,13 +172,14 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counters) {
 // max_norm, else 1. Summed in fp64, in an order that only the sizes decide:
 // each lane over its elements, each workgroup over its lanes, the workgroup
 // that finishes last over all partial sums.
-
 //
 // Bound by HBM: 512 workgroups of 512 threads, 16 KiB of a tensor each at a
 // time, two 16-byte loads in flight per lane, non-temporal: 186 us for
 // BERT-large's 1.34 GB in fp32 (7.2 TB/s), 99 us in bf16 (6.8 TB/s). 256 x
 // 1024 threads or 1024 x 256 of them took 191-198 us, one load in flight 284,
-// four 198.
+// four 198. What is left of a tensor after its whole tiles is summed element by
+// element (ResNet-50's 161 tensors: 19.1 us in fp32, 5.4 TB/s, 13.3 us in bf16,
+// 3.9 TB/s; 5000 tensors of 64 elements 7.2 us).
 constexpr int kNormThreads = 512;
 constexpr int kNormUnroll = 2;
 
@@ -442,6 +443,10 @@ struct StepValues {      // of the step, in registers
   uint32_t tile;         // low word of the tile's first group
 };
 
+// The replicas' addresses are read between the stores, which may alias them as
+// far as the compiler knows: each turn loads one and waits for it, and with it
+// for the store before (vmcnt counts both). Likely what separates ResNet-50 with
+// 8 replicas (5.9 TB/s in fp32, 5.4 with 8-bit states) from one (6.4 TB/s).
 template <int PD, bool MASTER, bool FULL>
 __device__ __forceinline__ void store_params(v4f w, const Tile& t, int i, const AdamwArgs& a) {
   const int left = t.len - i;
@@ -526,25 +531,30 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, t
 // How a step is cut into workgroups; none of them loops over tiles.
 //
 // 32-bit states are bound by HBM (28 bytes and some 45 instructions an
-// element). One wave and 256 elements per workgroup, 13 or 16 workgroups per
+// element). One wave and 256 elements per workgroup, 12 or 16 workgroups per
 // CU (each reserves its share of the LDS, which the kernel does not use): the
-// accesses of the whole GPU then move through every array in step. 13 where a
-// workgroup reads and writes 28 bytes an element (BERT-large, fp32: 1.44 ms,
-// 6.5 TB/s, against 1.46 with 16, 1.57 with 8 and 1.52 without the limit), 16
-// where it reads less (bf16 without masters: 1.12 ms against 1.16) or mostly
-// writes (ResNet-50, 8 replicas: 0.243 ms against 0.251). Other cuts of the
-// same case: workgroups of 256 threads at the same waves per CU 1.55, two
-// groups per lane 1.61, all workgroups of a tile on one XCD 1.66, workgroups
-// of 256 threads that loop over 4096 elements 1.68, and with plain loads and
-// stores 1.79.
+// accesses of the whole GPU then move through every array in step. 12 where a
+// workgroup reads and writes 28 bytes an element (BERT-large, fp32: 1.446 ms,
+// 6.5 TB/s, against 1.455 with 16, 1.57 with 8 and 1.52 without the limit; two
+// replicas 1.625 against 1.655), 16 where it reads less (bf16 without masters:
+// 1.125 ms against 1.151) or mostly writes, from five replicas on. At the
+// border, BERT-large in fp32, 12 against 16: R = 4 2.081 and 2.094 ms, R = 5
+// 2.327 and 2.312, R = 8 3.105 and 2.996; ResNet-50 R = 4 167.0 and 167.3 us,
+// R = 5 185.5 and 185.2, R = 8 246.6 and 243. (16-bit parameters with masters
+// would take 16 at R = 4 already: ResNet-50 149.5 and 143.0 us.) Other cuts of
+// BERT-large in fp32: workgroups of 256 threads at the same waves per CU 1.55,
+// two groups per lane 1.61, all workgroups of a tile on one XCD 1.66,
+// workgroups of 256 threads that loop over 4096 elements 1.68, and with plain
+// loads and stores 1.79.
 //
 // 8-bit states are bound by instructions nearly as much as by HBM (16 bytes
-// and some 47 instructions an element with fp32 parameters, 10 bytes in bf16):
-// the eight waves per SIMD that 64 registers allow, in workgroups of 256
-// threads, since each workgroup costs a start. Where the parameters are 16-bit
-// and have no master, two groups per lane: BERT-large 0.547 ms (6.2 TB/s)
-// against 0.592 with one and 0.566 with 7 waves; with fp32 parameters one:
-// 0.857 ms (6.3 TB/s) against 0.905 with two and 0.875 with 7 waves. The
+// and 52 instructions an element with fp32 parameters, 10 bytes and 54 in
+// bf16, the whole kernel's): the eight waves per SIMD that 64 registers allow,
+// in workgroups of 256 threads, since each workgroup costs a start. Where the
+// parameters are 16-bit and have no master, two groups per lane: BERT-large
+// 0.547 ms (6.2 TB/s) against 0.592 with one and 0.566 with 7 waves; with
+// fp32 parameters or masters one: 0.849 ms (6.3 TB/s) against 0.905 with two
+// and 0.875 with 7 waves, bf16 with masters 0.860 against 0.905 with two. The
 // scales in scalar loads, or the groups of several lanes per XCD, gained
 // nothing.
 template <int PD, bool MASTER, bool F8>
@@ -553,7 +563,8 @@ struct Shape {
   static constexpr int kU = adamw_unroll(PD, MASTER, F8);
   static constexpr int kPart = adamw_part(PD, MASTER, F8);
   static constexpr int kParts = kOptimTile / kPart;
-  static int lds(int R) { return F8 ? 0 : 160 * 1024 / ((PD != kF32 && !MASTER) || R > 4 ? 16 : 13); }
+  // Of 160 KiB, in pieces of 1280 bytes: 8 of them for 16 workgroups a CU, 10 for 12.
+  static int lds(int R) { return F8 ? 0 : 1280 * ((PD != kF32 && !MASTER) || R > 4 ? 8 : 10); }
   static constexpr int kWaves = F8 ? 8 : 1;                // per SIMD, at least
   static_assert(kParts * kPart == kOptimTile, "a tile is a whole number of parts");
 };

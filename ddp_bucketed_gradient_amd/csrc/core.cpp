@@ -49,6 +49,7 @@ int Reducer::bind(const BindArgs& args, std::string* err) {
   bound_ = (rc == kOk);
   bind_id_ = ++g_binds;
   averaged_ = true;
+  replays_ = false;
   static_bind_ = bound_ && args.no_alloc;
   sync_step_set_ = false;          // the launcher's tables were released
   // The launch log and the timing history refer to the previous binding's
@@ -82,7 +83,7 @@ int Reducer::check_idle(const char* what, std::string* err) const {
     *err = std::string(what) + ": a step is set for the coming synchronisation (ddpb_set_sync_step)";
     return kErrState;
   }
-  if (!averaged_) {
+  if (!averaged_ && !replays_ && plan_.R > 1) {     // one replica is its own average
     *err = std::string(what) + ": the gradients were written since the last synchronisation and are not averaged";
     return kErrState;
   }
@@ -252,6 +253,7 @@ int Reducer::finalize(std::string* err) {
   // every bucket's reduction, without a host synchronization.
   const int rc = launcher_->join(err);
   averaged_ = (rc == kOk);
+  replays_ = replays_ || launcher_->in_capture();
   log_ring_[finalized_ % kTimeRing] = log_;
   // a rebuild needs every variable's place in the ready order ([C30]: no
   // ready-order rebuild when the set of used parameters changes)

@@ -128,6 +128,8 @@ class Launcher {
   virtual int launch(int32_t first, int32_t last, int64_t iteration, std::string* err) = 0;
   // End of iteration: the compute stream waits for every side stream.
   virtual int join(std::string* err) = 0;
+  // Whether the compute stream is being captured into a graph.
+  virtual bool in_capture() = 0;
   virtual int accumulate(void* const* step_ptrs, int32_t step_dtype, bool first, std::string* err) = 0;
   // Device clock stamps of the given launched buckets (zeros when disabled).
   virtual int read_stamps(const std::vector<LaunchRecord>& log, std::vector<int64_t>* t0,
@@ -190,7 +192,7 @@ class Reducer {
   int64_t bind_id() const { return bound_ ? bind_id_ : 0; }
   // kErrState while an iteration is open (its buckets may still be reducing),
   // a step is set for the coming synchronisation, or the gradients have been
-  // written since the last one; kErrIncomplete while a failed one is latched.
+  // written since the last one (as far as the handle can know); kErrIncomplete while a failed one is latched.
   int check_idle(const char* what, std::string* err) const;
 
  private:
@@ -203,9 +205,12 @@ class Reducer {
   int64_t bind_id_ = 0;
   bool static_bind_ = false;       // bound by ddpb_bind_static: no staging for tables
   bool sync_ = true;
-  // As far as this handle can know: no local step, hook without synchronisation
-  // or unfinished iteration since the last synchronisation (or the bind).
+  // No local step, hook without synchronisation or unfinished iteration since
+  // the last synchronisation (or the bind).
   bool averaged_ = true;
+  // A synchronisation of this binding was captured: its replays, of which this
+  // handle learns nothing, average the gradients too.
+  bool replays_ = false;
   bool failed_ = false;            // latched "prior reduction did not finish"
   std::vector<int32_t> pending_;   // per bucket
   std::vector<uint8_t> ready_;     // per variable

@@ -1162,6 +1162,12 @@ class HipLauncher final : public Launcher {
     return kOk;
   }
 
+  bool in_capture() override {
+    bool cap = false;
+    std::string e;
+    return capturing(compute_, &cap, &e) == kOk && cap;
+  }
+
   int accumulate(void* const* step_ptrs, int32_t step_dtype, bool first, std::string* err) override {
     const HostRange range((flags_ & 4) != 0, "ddpb no_sync_accumulate");
     if (static_) {

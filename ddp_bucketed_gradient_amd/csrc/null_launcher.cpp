@@ -11,6 +11,8 @@ namespace {
 // Joins requested by every null launcher of the process (read by the host
 // tests through ddpb_hostonly_join_count).
 std::atomic<long long> g_joins{0};
+// Whether the null streams pretend to be captured (ddpb_hostonly_set_capture).
+std::atomic<int> g_capture{0};
 }  // namespace
 
 namespace ddpb {
@@ -24,6 +26,7 @@ class NullLauncher final : public Launcher {
     ++g_joins;
     return kOk;
   }
+  bool in_capture() override { return g_capture != 0; }
   int accumulate(void* const*, int32_t, bool, std::string*) override { return kOk; }
   int read_stamps(const std::vector<LaunchRecord>& log, std::vector<int64_t>* t0, std::vector<int64_t>* t1,
                   std::string*) override {
@@ -75,3 +78,7 @@ std::unique_ptr<Launcher> make_launcher() { return std::make_unique<NullLauncher
 // Host-only test build: how many times the state machine asked a launcher to
 // make the compute stream wait for the side streams.
 extern "C" long long ddpb_hostonly_join_count(void) { return g_joins.load(); }
+
+// Host-only test build: from here on the null launcher reports its stream as
+// being captured (or not).
+extern "C" void ddpb_hostonly_set_capture(int yes) { g_capture = yes; }

@@ -392,8 +392,10 @@ int ddpb_reset(ddpb_t h);
  * an iteration is open, once the reducer has been bound again, with a step set
  * for the coming synchronisation, and after ddpb_no_sync_accumulate, a hook
  * with synchronisation off or an iteration that was reset, until the next
- * synchronisation (DDPB_E_STATE), or while a failed iteration is latched
- * (DDPB_E_INCOMPLETE). Gradients that the caller wrote without telling the
+ * synchronisation, if R > 1 (DDPB_E_STATE), or while a failed iteration is latched
+ * (DDPB_E_INCOMPLETE). Once a synchronisation of the binding was captured into a
+ * graph, what was written since the last one is not held against it (a replay
+ * may have averaged it). Gradients that the caller wrote without telling the
  * reducer are not noticed. Pass the gradient addresses of one replica (they are
  * equal on all, but for the next case) and the reducer's compute stream.
  *

@@ -137,3 +137,40 @@ def test_a_variable_that_no_replica_used_takes_the_step_as_it_stands(view):
         # p's factor, product and difference (3 roundings of at most 1) and 13 of an update below lr
         assert (p.double() - want).abs().max().item() <= 2.0 ** -24 * (3 + 13 * 0.25)
     red.close()
+
+
+def test_local_steps_then_a_replayed_synchronisation_then_a_step():
+    """The synchronisation and the norm's and step's calls as a program mixes
+    them: local steps eagerly, the synchronisation as a graph, the step eagerly;
+    the same bits as with an eager synchronisation."""
+    shapes, R = [(1000,), (70,), (5000,)], 2
+    outs = []
+    for graph in (False, True):
+        gen = torch.Generator(device="cuda").manual_seed(5)
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            grads = [[torch.zeros(s, device="cuda") for s in shapes] for _ in range(R)]
+            steps = [[torch.zeros(s, device="cuda") for s in shapes] for _ in range(R)]
+            params = [torch.ones(s, device="cuda") for s in shapes]
+            red = D.Reducer(shapes, R, 4 * 3000)
+            red.bind(grads, compute_stream=stream)
+            opt, norm = red.adamw(params, lr=0.01), red.grad_norm()
+            if graph:
+                g = torch.cuda.CUDAGraph()
+                stream.synchronize()
+                with torch.cuda.graph(g, stream=stream):
+                    red.sync()
+            for _ in range(3):
+                for first in (True, False):
+                    for row in steps:
+                        for t in row:
+                            t.copy_(torch.randn(t.shape, generator=gen, device="cuda"))
+                    red.no_sync_accumulate(steps, first_step=first)
+                g.replay() if graph else red.sync()
+                norm.compute(max_norm=0.5)
+                opt.step(clip=norm)
+            stream.synchronize()
+            outs.append([raw(t) for t in params + grads[0] + grads[1]])
+        red.close()
+    for a, b in zip(*outs):
+        assert np.array_equal(a, b)

@@ -144,3 +144,40 @@ def test_a_new_binding_starts_afresh(bound):
     bound.bind()                                              # other gradients, of which nothing is known
     bound.handles()
     assert bound.codes() == D.OK
+
+
+def test_replays_of_a_captured_synchronisation(bound):
+    """Local steps cannot be captured, the synchronisation that follows them can:
+    the handle learns nothing of its replays, so that on a binding with a
+    captured one written gradients may have been averaged since."""
+    bound.lib.dll.ddpb_hostonly_set_capture(1)
+    bound.red.sync()
+    bound.lib.dll.ddpb_hostonly_set_capture(0)
+    assert bound.codes() == D.OK
+    bound.accumulate()
+    bound.accumulate(first=False)
+    assert bound.codes() == D.OK                              # behind a replay, for all the handle knows
+    bound.red.mark_ready(2)
+    assert bound.codes() == D.E_STATE                         # an iteration of its own it knows of
+    bound.red.mark_ready_many([1, 0])
+    bound.red.finalize()
+    assert bound.codes() == D.OK
+    bound.bind()
+    bound.handles()
+    bound.accumulate()
+    assert bound.codes() == D.E_STATE                         # the graphs went with the binding
+
+
+def test_one_replica_is_its_own_average(host):  # noqa: F811
+    red = D.Reducer([(10,)], 1, 0, lib=host)
+    red.bind_ptrs([0x1000], side_streams=[0])
+    n = host.norm_create([10], [D.F32])
+    host.norm_bind(n, [0x10000], 0x100, host.norm_workspace_bytes(n), 0, red.h)
+    host.no_sync_accumulate(red.h, [0x2000], D.F32, True)
+    host.norm_compute(n, 1.0, reducer=red.h)
+    host.set_sync_step(red.h, [0x2000], D.F32, False)         # not in the gradient yet
+    assert _code(lambda: host.norm_compute(n, 1.0, reducer=red.h)) == D.E_STATE
+    red.sync()
+    host.norm_compute(n, 1.0, reducer=red.h)
+    host.norm_destroy(n)
+    red.close()

@@ -54,7 +54,10 @@ def _check(ts, what: str, numels, dtype, device) -> list:
 
 
 class _Handle:
-    """A native handle with its workspace, bound to one stream of one device."""
+    """A native handle with its workspace, bound to one stream of one device.
+
+    A graph that captured its calls uses its memory: the object has to live as
+    long as the graph is replayed."""
     _destroy = ""
 
     def _open(self, lib, h, device, stream, reducer):

@@ -323,7 +323,8 @@ __device__ __forceinline__ uint32_t encode4(v4f x, uint32_t top, v4u random, uin
   const uint32_t bits = max(top + 0x1FFFFFu, static_cast<uint32_t>(9 + SHIFT) << 23) - (8u << 23);
   *scale = (bits >> 23) - SHIFT;
   const float f = as_float(bits & kInf);
-  // fmed3: with x = 0, 0 is the middle one; else x 2^127 is over `least` < 2^48 (of all x >= 2^-63, which did not underflow)
+  // fmed3: with x = 0, 0 is the middle one; else x 2^127 is over `least` < 2^48
+  // (for all x >= 2^-63, which did not underflow).
   const float least = f * 0x1p-9f;
   int codes = 0;
 #define DDPB_SR(J)                                                                                     \
@@ -477,11 +478,12 @@ __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, f
 // 8-bit states. m and v are rounded operation by operation, as in the 32-bit
 // step (one rounding more or less would move a code here and there); in the
 // parameter's update products are fused into the sums they feed. v and r are
-// carried as 2^64 v and 2^32 r, which keeps v normal for roots down to 2^-95 (below,
-// fast_sqrt lets them underflow gradually); what then overflows (r > 4e9), or is not finite, takes the
-// way without shortcuts, and with an eps outside fast_div's range everything
-// does. A whole wave goes that way, in which the elements that need none of it
-// keep what they have: none depends on what lies beside it.
+// carried as 2^64 v and 2^32 r, which keeps v normal for roots down to 2^-95
+// (below, fast_sqrt lets them underflow gradually). What then overflows (r >
+// 4e9), or is not finite, takes the way without shortcuts, and with an eps
+// outside fast_div's range everything does. A whole wave goes that way, in which
+// the elements that need none of it keep what they have: none depends on what
+// lies beside it.
 template <int PD, int GD, bool MASTER, bool FULL>
 __device__ __forceinline__ void update_quad(const Quad<MASTER ? kF32 : PD, GD, true>& q, const Tile& t, int at,
                                             int lane4, const AdamwArgs& a, const StepValues& s) {

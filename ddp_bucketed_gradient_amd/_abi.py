@@ -42,6 +42,9 @@ SYMBOLS = [
     "ddpb_norm_create", "ddpb_norm_destroy", "ddpb_norm_workspace_bytes", "ddpb_norm_bind", "ddpb_norm_compute",
     "ddpb_adamw_create", "ddpb_adamw_destroy", "ddpb_adamw_workspace_bytes", "ddpb_adamw_bind", "ddpb_adamw_step",
     "ddpb_adamw_set_step", "ddpb_adamw_get_step",
+    "ddpb_check_writable", "ddpb_dropout", "ddpb_layer_norm", "ddpb_layer_norm_backward",
+    "ddpb_layer_norm_backward_workspace_bytes", "ddpb_embedding", "ddpb_embedding_backward",
+    "ddpb_embedding_backward_workspace_bytes",
 ]
 
 
@@ -54,6 +57,11 @@ class DdpbError(RuntimeError):
 i32, i64, vp, f64 = C.c_int32, C.c_int64, C.c_void_p, C.c_double
 PF64 = C.POINTER(C.c_double)
 P32, P64 = C.POINTER(C.c_int32), C.POINTER(C.c_int64)
+
+
+class DropStruct(C.Structure):
+    """ddpb_drop"""
+    _fields_ = [("p", f64), ("seed", C.c_uint64), ("offset", C.c_uint64), ("offset_device", vp)]
 
 
 def ptr_array(ptrs: Sequence[int]):
@@ -106,6 +114,15 @@ def _sig(lib):
         "ddpb_adamw_step": [vp, vp, f64, vp, f64, vp],
         "ddpb_adamw_set_step": [vp, i64],
         "ddpb_adamw_get_step": [vp, P64],
+        "ddpb_check_writable": [vp, i32],
+        "ddpb_dropout": [i64, i64, i32, vp, i64, vp, i64, C.POINTER(DropStruct), vp, vp],
+        "ddpb_layer_norm": [i64, i64, i32, vp, i64, vp, i64, C.POINTER(DropStruct), vp, vp, i32, f64, vp, vp, vp, vp],
+        "ddpb_layer_norm_backward_workspace_bytes": [i64, i64, P64],
+        "ddpb_layer_norm_backward": [i64, i64, i32, vp, i64, vp, i64, vp, vp, i64, C.POINTER(DropStruct), vp, i32, vp,
+                                     vp, vp, vp, i32, i32, vp, i64, vp],
+        "ddpb_embedding": [i64, vp, i32, i64, i64, vp, i32, f64, vp, i64, vp, i32, vp],
+        "ddpb_embedding_backward_workspace_bytes": [i64, i64, i64, P64],
+        "ddpb_embedding_backward": [i64, vp, i32, i64, i64, vp, i64, i32, f64, vp, i32, i32, vp, i64, vp],
         "ddpb_last_error": [],
     }
     for name, args in S.items():
@@ -294,6 +311,56 @@ class Lib:
         t = i64()
         self._check(self.dll.ddpb_adamw_get_step(a, C.byref(t)))
         return t.value
+
+    # -- beside the matrix products -----------------------------------------------------
+    # addresses are integers, 0 for NULL; drop: a DropStruct or None
+    def check_writable(self, h, v: int):
+        self._check(self.dll.ddpb_check_writable(h, v))
+
+    def dropout(self, rows, cols, dtype, x, x_stride, residual, residual_stride, drop, y, stream):
+        rc = self.dll.ddpb_dropout(rows, cols, dtype, x, x_stride, residual, residual_stride, drop, y, stream)
+        if rc != OK:
+            raise DdpbError(rc, self.last_error())
+
+    def layer_norm(self, rows, cols, dtype, x, x_stride, residual, residual_stride, drop, weight, bias, weight_dtype,
+                   eps, y, h, stats, stream):
+        rc = self.dll.ddpb_layer_norm(rows, cols, dtype, x, x_stride, residual, residual_stride, drop, weight, bias,
+                                      weight_dtype, eps, y, h, stats, stream)
+        if rc != OK:
+            raise DdpbError(rc, self.last_error())
+
+    def layer_norm_backward_workspace_bytes(self, rows, cols) -> int:
+        b = i64()
+        self._check(self.dll.ddpb_layer_norm_backward_workspace_bytes(rows, cols, C.byref(b)))
+        return b.value
+
+    def layer_norm_backward(self, rows, cols, dtype, dy, dy_stride, h, h_stride, stats, grad_h, grad_h_stride, drop,
+                            weight, weight_dtype, dh, dx, dweight, dbias, grad_dtype, accumulate, workspace, ws_bytes,
+                            stream):
+        rc = self.dll.ddpb_layer_norm_backward(rows, cols, dtype, dy, dy_stride, h, h_stride, stats, grad_h,
+                                               grad_h_stride, drop, weight, weight_dtype, dh, dx, dweight, dbias,
+                                               grad_dtype, 1 if accumulate else 0, workspace, ws_bytes, stream)
+        if rc != OK:
+            raise DdpbError(rc, self.last_error())
+
+    def embedding(self, n, tokens, token_bytes, vocab, cols, table, table_dtype, scale, residual, residual_stride, y,
+                  dtype, stream):
+        rc = self.dll.ddpb_embedding(n, tokens, token_bytes, vocab, cols, table, table_dtype, scale, residual,
+                                     residual_stride, y, dtype, stream)
+        if rc != OK:
+            raise DdpbError(rc, self.last_error())
+
+    def embedding_backward_workspace_bytes(self, n, vocab, cols) -> int:
+        b = i64()
+        self._check(self.dll.ddpb_embedding_backward_workspace_bytes(n, vocab, cols, C.byref(b)))
+        return b.value
+
+    def embedding_backward(self, n, tokens, token_bytes, vocab, cols, dy, dy_stride, dtype, scale, dtable, grad_dtype,
+                           accumulate, workspace, ws_bytes, stream):
+        rc = self.dll.ddpb_embedding_backward(n, tokens, token_bytes, vocab, cols, dy, dy_stride, dtype, scale,
+                                              dtable, grad_dtype, 1 if accumulate else 0, workspace, ws_bytes, stream)
+        if rc != OK:
+            raise DdpbError(rc, self.last_error())
 
     # -- diagnostics ------------------------------------------------------------------
     def get_launch_log(self, h, with_stamps: bool = False):

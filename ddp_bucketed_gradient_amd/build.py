@@ -17,6 +17,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +28,7 @@ HIP_LIB = os.path.join(LIBDIR, "libddpb.so")
 HOST_LIB = os.path.join(LIBDIR, "libddpb_hostonly.so")
 ARCH = "gfx950"
 
-HOST_SOURCES = ["plan.cpp", "core.cpp", "optim.cpp", "abi.cpp"]
+HOST_SOURCES = ["plan.cpp", "core.cpp", "optim.cpp", "layers.cpp", "abi.cpp"]
 
 # -ffp-contract=off: no fused multiply-add may change the rounding of the mean.
 # packed-fp32-ops disabled: the float4 adds stay scalar v_add_f32.
@@ -49,10 +51,15 @@ def _run(cmd):
 
 
 def build_hip(out: str = HIP_LIB) -> str:
+    """One object for each source, compiled side by side, then linked."""
     os.makedirs(os.path.dirname(out), exist_ok=True)
-    srcs = [os.path.join(CSRC, s) for s in HOST_SOURCES + ["kernels.hip", "optim.hip"]]
+    srcs = [os.path.join(CSRC, s) for s in HOST_SOURCES + ["kernels.hip", "optim.hip", "layers.hip", "embedding.hip"]]
     tmp = out + ".tmp"
-    _run([_hipcc()] + HIPCC_FLAGS + srcs + ["-L/opt/rocm/lib", "-lrocprofiler-sdk-roctx", "-o", tmp])
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as at, ThreadPoolExecutor(min(len(srcs), os.cpu_count() or 1, 8)) as pool:
+        objs = [os.path.join(at, os.path.basename(s) + ".o") for s in srcs]
+        list(pool.map(lambda so: _run([_hipcc()] + flags + ["-c", so[0], "-o", so[1]]), zip(srcs, objs)))
+        _run([_hipcc()] + HIPCC_FLAGS + objs + ["-L/opt/rocm/lib", "-lrocprofiler-sdk-roctx", "-o", tmp])
     os.replace(tmp, out)
     return out
 

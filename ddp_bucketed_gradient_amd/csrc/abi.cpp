@@ -10,6 +10,7 @@
 
 #include "../../include/ddpb.h"
 #include "core.hpp"
+#include "layers.hpp"
 #include "optim.hpp"
 
 struct ddpb_reducer {
@@ -64,6 +65,23 @@ int guarded(const char* what, F f) {
   } catch (const std::exception&) {
     return fail(DDPB_E_NOMEM, std::string(what) + ": out of host memory");
   }
+}
+
+// Builds the kernels' arguments, checks them and enqueues the call.
+template <typename Args, typename Fill>
+int enqueue(const char* what, int (ddpb::LayersDevice::*call)(const Args&, std::string*), Fill fill) {
+  return guarded(what, [&](std::string* err) {
+    Args a;
+    int rc = fill(&a, err);
+    if (rc == DDPB_OK) rc = ddpb::check(a, err);
+    return rc == DDPB_OK ? (ddpb::layers_device()->*call)(a, err) : rc;
+  });
+}
+
+int drop_of(const ddpb_drop* d, ddpb::DropSpec* out, const char* what, std::string* err) {
+  if (d == nullptr) return DDPB_OK;
+  const ddpb::DropArgs a{d->p, d->seed, d->offset, d->offset_device};
+  return ddpb::make_drop(&a, out, what, err);
 }
 }  // namespace
 
@@ -510,6 +528,142 @@ int ddpb_adamw_set_step(ddpb_adamw_t a, int64_t step) {
 int ddpb_adamw_get_step(ddpb_adamw_t a, int64_t* step) {
   if (!a || !step) return fail(DDPB_E_ARG, "adamw get_step: NULL argument");
   return guarded("adamw get_step", [&](std::string* err) { return a->opt.get_step(step, err); });
+}
+
+int ddpb_check_writable(ddpb_t h, int32_t v) {
+  if (!h) return fail(DDPB_E_ARG, "check_writable: NULL handle");
+  std::string err;
+  return pass(h->red.check_writable(v, &err), err);
+}
+
+int ddpb_layer_norm(int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                    int64_t residual_stride, const ddpb_drop* drop, const void* weight, const void* bias,
+                    int32_t weight_dtype, double eps, void* y, void* h, float* stats, void* stream) {
+  if (!is_dtype(dtype) || !is_dtype(weight_dtype)) return fail(DDPB_E_ARG, "layer_norm: bad dtype");
+  return enqueue("layer_norm", &ddpb::LayersDevice::norm_forward, [&](ddpb::NormForwardArgs* a, std::string* err) {
+    a->rows = rows;
+    a->cols = cols;
+    a->dtype = dtype;
+    a->weight_dtype = weight_dtype;
+    a->x = {x, x_stride};
+    a->residual = {residual, residual_stride};
+    a->weight = weight;
+    a->bias = bias;
+    a->eps = eps;
+    a->y = y;
+    a->h = h;
+    a->stats = stats;
+    a->stream = stream;
+    return drop_of(drop, &a->drop, "layer_norm", err);
+  });
+}
+
+int ddpb_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int64_t* bytes) {
+  if (bytes == nullptr || !ddpb::norm_sizes_ok(rows, cols))
+    return fail(DDPB_E_ARG, "layer_norm_backward workspace_bytes: bad argument");
+  *bytes = ddpb::norm_backward_workspace(rows, cols);
+  return DDPB_OK;
+}
+
+int ddpb_layer_norm_backward(int64_t rows, int64_t cols, int32_t dtype, const void* dy, int64_t dy_stride,
+                             const void* h, int64_t h_stride, const float* stats, const void* grad_h,
+                             int64_t grad_h_stride, const ddpb_drop* drop, const void* weight, int32_t weight_dtype,
+                             void* dh, void* dx, void* dweight, void* dbias, int32_t grad_dtype, int32_t accumulate,
+                             void* workspace, int64_t ws_bytes, void* stream) {
+  if (!is_dtype(dtype) || !is_dtype(weight_dtype) || !is_dtype(grad_dtype))
+    return fail(DDPB_E_ARG, "layer_norm_backward: bad dtype");
+  return enqueue("layer_norm_backward", &ddpb::LayersDevice::norm_backward,
+                 [&](ddpb::NormBackwardArgs* a, std::string* err) {
+    a->rows = rows;
+    a->cols = cols;
+    a->dtype = dtype;
+    a->weight_dtype = weight_dtype;
+    a->grad_dtype = grad_dtype;
+    a->dy = {dy, dy_stride};
+    a->h = {h, h_stride};
+    a->grad_h = {grad_h, grad_h_stride};
+    a->stats = stats;
+    a->weight = weight;
+    a->dh = dh;
+    a->dx = dx;
+    a->dweight = dweight;
+    a->dbias = dbias;
+    a->accumulate = accumulate != 0;
+    a->workspace = workspace;
+    a->ws_bytes = ws_bytes;
+    a->stream = stream;
+    return drop_of(drop, &a->drop, "layer_norm_backward", err);
+  });
+}
+
+int ddpb_dropout(int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                 int64_t residual_stride, const ddpb_drop* drop, void* y, void* stream) {
+  if (!is_dtype(dtype)) return fail(DDPB_E_ARG, "dropout: bad dtype");
+  if (drop == nullptr) return fail(DDPB_E_ARG, "dropout: drop is NULL");
+  return enqueue("dropout", &ddpb::LayersDevice::dropout, [&](ddpb::DropoutArgs* a, std::string* err) {
+    a->rows = rows;
+    a->cols = cols;
+    a->dtype = dtype;
+    a->x = {x, x_stride};
+    a->residual = {residual, residual_stride};
+    a->y = y;
+    a->stream = stream;
+    return drop_of(drop, &a->drop, "dropout", err);
+  });
+}
+
+int ddpb_embedding(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols, const void* table,
+                   int32_t table_dtype, double scale, const void* residual, int64_t residual_stride, void* y,
+                   int32_t dtype, void* stream) {
+  if (!is_dtype(dtype) || !is_dtype(table_dtype) || (token_bytes != 4 && token_bytes != 8))
+    return fail(DDPB_E_ARG, "embedding: bad dtype or token_bytes");
+  return enqueue("embedding", &ddpb::LayersDevice::lookup, [&](ddpb::LookupArgs* a, std::string*) {
+    a->n = n;
+    a->vocab = vocab;
+    a->cols = cols;
+    a->tokens = tokens;
+    a->token_bytes = token_bytes;
+    a->table = table;
+    a->table_dtype = table_dtype;
+    a->scale = static_cast<float>(scale);
+    a->residual = {residual, residual_stride};
+    a->y = y;
+    a->dtype = dtype;
+    a->stream = stream;
+    return DDPB_OK;
+  });
+}
+
+int ddpb_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t cols, int64_t* bytes) {
+  if (bytes == nullptr || !ddpb::lookup_sizes_ok(n, vocab, cols))
+    return fail(DDPB_E_ARG, "embedding_backward workspace_bytes: bad argument");
+  *bytes = ddpb::lookup_plan(n, vocab, cols).bytes;
+  return DDPB_OK;
+}
+
+int ddpb_embedding_backward(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols,
+                            const void* dy, int64_t dy_stride, int32_t dtype, double scale, void* dtable,
+                            int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t ws_bytes, void* stream) {
+  if (!is_dtype(dtype) || !is_dtype(grad_dtype) || (token_bytes != 4 && token_bytes != 8))
+    return fail(DDPB_E_ARG, "embedding_backward: bad dtype or token_bytes");
+  return enqueue("embedding_backward", &ddpb::LayersDevice::lookup_backward,
+                 [&](ddpb::LookupBackwardArgs* a, std::string*) {
+    a->n = n;
+    a->vocab = vocab;
+    a->cols = cols;
+    a->tokens = tokens;
+    a->token_bytes = token_bytes;
+    a->dy = {dy, dy_stride};
+    a->dtype = dtype;
+    a->grad_dtype = grad_dtype;
+    a->scale = static_cast<float>(scale);
+    a->dtable = dtable;
+    a->accumulate = accumulate != 0;
+    a->workspace = workspace;
+    a->ws_bytes = ws_bytes;
+    a->stream = stream;
+    return DDPB_OK;
+  });
 }
 
 }  // extern "C"

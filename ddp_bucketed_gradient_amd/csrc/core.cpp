@@ -90,6 +90,38 @@ int Reducer::check_idle(const char* what, std::string* err) const {
   return kOk;
 }
 
+int Reducer::check_writable(int32_t v, std::string* err) const {
+  if (!bound_) {
+    *err = "check_writable: reducer is not bound";
+    return kErrState;
+  }
+  if (v < 0 || v >= plan_.P) {
+    *err = "check_writable: variable index out of range";
+    return kErrIndex;
+  }
+  if (failed_) {
+    *err = "check_writable: the previous iteration left buckets unreduced; call ddpb_reset first";
+    return kErrIncomplete;
+  }
+  if (sync_step_set_) {
+    *err = "check_writable: a step is set for the coming synchronisation, which adds it to the gradients";
+    return kErrState;
+  }
+  if (sync_ && used_set_) {
+    bool used = false;
+    for (int32_t r = 0; r < plan_.R; ++r) used = used || used_acc_[static_cast<size_t>(r) * plan_.P + v] != 0;
+    if (!used) {
+      *err = "check_writable: no replica uses this variable in the coming synchronisation";
+      return kErrState;
+    }
+  }
+  if (sync_ && started_ && ready_[v]) {
+    *err = "check_writable: the variable is marked ready already, its bucket may be reducing";
+    return kErrDoubleReady;
+  }
+  return kOk;
+}
+
 int Reducer::mark_ready(int32_t v, std::string* err) {
   if (!bound_) {
     *err = "mark_ready: reducer is not bound";

@@ -194,6 +194,11 @@ class Reducer {
   // a step is set for the coming synchronisation, or the gradients have been
   // written since the last one (as far as the handle can know); kErrIncomplete while a failed one is latched.
   int check_idle(const char* what, std::string* err) const;
+  // Whether a backward pass may write variable v's gradients now: kErrState
+  // while unbound, with a step set for the coming synchronisation or with v
+  // unused in it, kErrIndex, kErrIncomplete while a failed iteration is latched,
+  // kErrDoubleReady once v is ready (its bucket may be reducing).
+  int check_writable(int32_t v, std::string* err) const;
 
  private:
   void begin_iteration();

@@ -1,10 +1,11 @@
-// null_launcher.cpp -- Launcher and OptimDevice that enqueue nothing. Linked only into the
+// null_launcher.cpp -- Launcher, OptimDevice and LayersDevice that enqueue nothing. Linked only into the
 // host-only test library so the plan and the readiness state machine can be
 // exercised on a machine without a GPU. It moves no data: gradients are left
 // untouched, so it is never a substitute for the HIP launcher.
 #include <atomic>
 
 #include "core.hpp"
+#include "layers.hpp"
 #include "optim.hpp"
 
 namespace {
@@ -64,7 +65,21 @@ class NullOptimDevice final : public OptimDevice {
   int adamw(const AdamwLaunch&, std::string*) override { return kOk; }
 };
 
+class NullLayersDevice final : public LayersDevice {
+ public:
+  int norm_forward(const NormForwardArgs&, std::string*) override { return kOk; }
+  int norm_backward(const NormBackwardArgs&, std::string*) override { return kOk; }
+  int dropout(const DropoutArgs&, std::string*) override { return kOk; }
+  int lookup(const LookupArgs&, std::string*) override { return kOk; }
+  int lookup_backward(const LookupBackwardArgs&, std::string*) override { return kOk; }
+};
+
 }  // namespace
+
+LayersDevice* layers_device() {
+  static NullLayersDevice d;
+  return &d;
+}
 
 OptimDevice* optim_device() {
   static NullOptimDevice d;

@@ -1,0 +1,256 @@
+"""Python front end of the operators beside a model's matrix products
+(``include/ddpb.h``, "Beside the matrix products"): layer norm, dropout and the
+embedding, each with its backward pass.
+
+As elsewhere, PyTorch supplies device memory and streams and every step runs in
+the native library. The functions work like torch's own: on the current stream
+of the tensors' device, with outputs and workspaces from torch's allocator, so
+they can be captured into graphs. They record nothing for autograd: the backward
+passes are called by name and write the parameters' gradients where they are
+told to, such as the tensors a Reducer is bound to.
+"""
+from __future__ import annotations
+
+import math as _math
+from typing import NamedTuple, Optional
+
+from . import _abi
+from .optim import _code
+
+
+class Drop:
+    """Which elements a dropout keeps: a function of the seed, the offset and an
+    element's index, so that nothing is stored for the backward pass, which
+    takes the same Drop. Each dropout of a step needs an offset of its own.
+
+    ``p``: the share that is dropped, rounded to a multiple of 2^-16 (what is
+    kept is scaled by just that share). ``counter``: None, or a 1-element int64
+    CUDA tensor that is added to the offset when a call runs, so that a replayed
+    graph drops anew once the counter has moved (behind the backward pass); it
+    has to live as long as such a graph.
+    """
+    __slots__ = ("p", "seed", "offset", "counter", "active", "_c")
+
+    def __init__(self, p: float, seed: int, offset: int = 0, counter=None):
+        p = float(p)
+        if not 0.0 <= p <= 1.0:
+            raise ValueError("p must be in [0, 1]")
+        at = None
+        if counter is not None:
+            import torch
+            if not isinstance(counter, torch.Tensor) or counter.dtype != torch.int64 or not counter.is_cuda \
+                    or counter.numel() != 1:
+                raise ValueError("counter must be a 1-element int64 CUDA tensor")
+            at = counter.data_ptr()
+        m = (1 << 64) - 1
+        self.p, self.seed, self.offset, self.counter = p, int(seed), int(offset), counter
+        self.active = _math.floor(p * 65536 + 0.5) > 0
+        self._c = _abi.DropStruct(p, self.seed & m, self.offset & m, at)
+
+    def _on(self, device):
+        if self.counter is not None and self.counter.device != device:
+            raise ValueError(f"the dropout's counter must be on {device}")
+        return self._c
+
+    def __repr__(self):
+        return f"Drop(p={self.p}, seed={self.seed}, offset={self.offset}, counter={self.counter})"
+
+
+class Normed(NamedTuple):
+    """What layer_norm returns: y; h, the input of the norm (x itself without
+    residual and dropout); stats, fp32, mean and 1 / deviation of each row."""
+    y: object
+    h: object
+    stats: object
+
+
+class NormGrads(NamedTuple):
+    """What layer_norm_backward returns: the gradient of x, and that of h, which
+    is the residual's (the same tensor without a dropout)."""
+    dx: object
+    dh: object
+
+
+def _rows(t, what: str, like=None):
+    """(rows, cols, stride) of a CUDA tensor whose rows, of its last dimension,
+    lie at equal distances. ``like``: a tensor of the same shape, type and device."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{what} must have shape {tuple(like.shape)} and type {like.dtype} on {like.device}")
+    if t.dim() == 0:
+        raise ValueError(f"{what} must have at least one dimension")
+    cols, n = t.shape[-1], t.numel()
+    if t.is_contiguous():
+        return (n // cols if cols else _math.prod(t.shape[:-1])), cols, cols
+    if cols != 1 and t.stride(-1) != 1:
+        raise ValueError(f"the elements of a row of {what} must be consecutive")
+    stride = size = None
+    for n_d, s_d in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n_d == 1:
+            continue
+        if stride is None:
+            stride, size = s_d, n_d
+        elif s_d != stride * size:
+            raise ValueError(f"the rows of {what} must lie at equal distances: call contiguous() first")
+        else:
+            size *= n_d
+    return n // cols, cols, cols if stride is None else stride
+
+
+def _vector(t, what: str, n: int, device, dtype=None):
+    """The address of an optional contiguous tensor of n elements."""
+    if t is None:
+        return 0
+    if not t.is_cuda or t.device != device or not t.is_contiguous() or t.numel() != n or \
+            (dtype is not None and t.dtype != dtype):
+        kind = "" if dtype is None else f"{dtype} "
+        raise ValueError(f"{what} must be a contiguous {kind}CUDA tensor of {n} elements on {device}")
+    return t.data_ptr()
+
+
+def _call(device, f, *args):
+    """f(*args, stream) on the current stream of ``device``."""
+    import torch
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        return f(*args, stream)
+    with torch.cuda.device(device):
+        return f(*args, stream)
+
+
+def _wrote(*ts):
+    """The gradients were written in place, through their addresses: autograd
+    counts writes by tensor."""
+    import torch
+    for t in ts:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
+def _lib(lib):
+    return lib if lib is not None else _abi.lib()
+
+
+def dropout(x, drop: Drop, residual=None, lib: Optional[_abi.Lib] = None):
+    """``x`` with a share of its elements dropped and the others scaled, plus
+    ``residual``. Contiguous, of x's type (fp32, bf16 or fp16)."""
+    import torch
+    code = _code(x.dtype, "x")
+    rows, cols, stride = _rows(x, "x")
+    rs = 0 if residual is None else _rows(residual, "residual", x)[2]
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _call(x.device, _lib(lib).dropout, rows, cols, code, x.data_ptr(), stride,
+          0 if residual is None else residual.data_ptr(), rs, drop._on(x.device), y.data_ptr())
+    return y
+
+
+def dropout_backward(dy, drop: Drop, lib: Optional[_abi.Lib] = None):
+    """The gradient of dropout's x (the residual's is dy)."""
+    return dropout(dy, drop, lib=lib)
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, drop: Optional[Drop] = None,
+               lib: Optional[_abi.Lib] = None) -> Normed:
+    """Layer norm over the last dimension of ``h = residual + dropout(x)``, in
+    one pass. ``weight`` and ``bias``: one type, which may differ from x's."""
+    import torch
+    code, dev = _code(x.dtype, "x"), x.device
+    rows, cols, stride = _rows(x, "x")
+    rs = 0 if residual is None else _rows(residual, "residual", x)[2]
+    wt = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
+    w, b = _vector(weight, "weight", cols, dev, wt), _vector(bias, "bias", cols, dev, wt)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    fused = residual is not None or (drop is not None and drop.active)
+    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if fused else x
+    stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=dev)
+    _call(dev, _lib(lib).layer_norm, rows, cols, code, x.data_ptr(), stride,
+          0 if residual is None else residual.data_ptr(), rs, None if drop is None else drop._on(dev), w, b,
+          _code(wt, "weight and bias"), eps, y.data_ptr(), h.data_ptr() if fused else 0, stats.data_ptr())
+    return Normed(y, h, stats)
+
+
+def layer_norm_backward(dy, h, stats, weight=None, dweight=None, dbias=None, grad_h=None,
+                        drop: Optional[Drop] = None, accumulate: bool = False,
+                        lib: Optional[_abi.Lib] = None) -> NormGrads:
+    """The gradients of layer_norm. ``h``, ``stats``: what it returned; ``drop``:
+    the one it was called with. ``dweight``, ``dbias`` (any of them None if not
+    wanted; one type): written, or with ``accumulate`` added to. ``grad_h``: a
+    gradient that reaches h from elsewhere, as where h itself goes on as the
+    next residual."""
+    import torch
+    code, dev = _code(dy.dtype, "dy"), dy.device
+    rows, cols, stride = _rows(dy, "dy")
+    hs = _rows(h, "h", dy)[2]
+    gs = 0 if grad_h is None else _rows(grad_h, "grad_h", dy)[2]
+    st = _vector(stats, "stats", 2 * rows, dev, torch.float32)
+    w = _vector(weight, "weight", cols, dev)
+    gt = dweight.dtype if dweight is not None else dbias.dtype if dbias is not None else torch.float32
+    dw, db = _vector(dweight, "dweight", cols, dev, gt), _vector(dbias, "dbias", cols, dev, gt)
+    lib = _lib(lib)
+    ws = None
+    if dw or db:
+        ws = torch.empty(lib.layer_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
+    dh = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    dropped = drop is not None and drop.active
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dev) if dropped else dh
+    _call(dev, lib.layer_norm_backward, rows, cols, code, dy.data_ptr(), stride, h.data_ptr(), hs, st,
+          0 if grad_h is None else grad_h.data_ptr(), gs, drop._on(dev) if dropped else None, w,
+          code if weight is None else _code(weight.dtype, "weight"), dh.data_ptr(), dx.data_ptr() if dropped else 0,
+          dw, db, _code(gt, "dweight and dbias"), accumulate, 0 if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
+    _wrote(dweight, dbias)
+    return NormGrads(dx, dh)
+
+
+def _tokens(tokens, device):
+    """(count, address, bytes) of a tensor of tokens."""
+    import torch
+    size = {torch.int64: 8, torch.int32: 4}.get(tokens.dtype)
+    if size is None or not tokens.is_cuda or tokens.device != device or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous int64 or int32 CUDA tensor on {device}")
+    return tokens.numel(), tokens.data_ptr(), size
+
+
+def _table(t, what: str):
+    if t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA tensor of two dimensions")
+    return t.shape[0], t.shape[1], _code(t.dtype, what)
+
+
+def embedding(tokens, table, scale: float = 1.0, residual=None, dtype=None, lib: Optional[_abi.Lib] = None):
+    """``scale * table[tokens] + residual``, of the table's type or ``dtype``. A
+    token outside of the table gives a row of zeros."""
+    import torch
+    vocab, cols, tc = _table(table, "table")
+    dev = table.device
+    n, at, size = _tokens(tokens, dev)
+    dtype = table.dtype if dtype is None else dtype
+    code = _code(dtype, "dtype")
+    y = torch.empty(tokens.shape + (cols,), dtype=dtype, device=dev)
+    rs = 0 if residual is None else _rows(residual, "residual", y)[2]
+    _call(dev, _lib(lib).embedding, n, at, size, vocab, cols, table.data_ptr(), tc, scale,
+          0 if residual is None else residual.data_ptr(), rs, y.data_ptr(), code)
+    return y
+
+
+def embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bool = False,
+                       lib: Optional[_abi.Lib] = None):
+    """The gradient of embedding's table (the residual's is dy): row v of
+    ``dtable`` becomes ``scale`` times the sum of dy over the places of token v,
+    in their order; with ``accumulate`` that is added to it. Tokens outside of the
+    table are left out. Returns dtable."""
+    import torch
+    vocab, cols, gc = _table(dtable, "dtable")
+    dev = dtable.device
+    n, at, size = _tokens(tokens, dev)
+    if dy.device != dev or dy.shape != tokens.shape + (cols,):
+        raise ValueError(f"dy must have shape {tuple(tokens.shape) + (cols,)} on {dev}")
+    stride = _rows(dy, "dy")[2]
+    code = _code(dy.dtype, "dy")
+    lib = _lib(lib)
+    ws = torch.empty(lib.embedding_backward_workspace_bytes(n, vocab, cols), dtype=torch.uint8, device=dev)
+    _call(dev, lib.embedding_backward, n, at, size, vocab, cols, dy.data_ptr(), stride, code, scale,
+          dtable.data_ptr(), gc, accumulate, ws.data_ptr(), ws.numel())
+    _wrote(dtable)
+    return dtable

@@ -13,6 +13,7 @@ from typing import List, Optional, Sequence
 from . import _abi
 from ._abi import (BF16, F32, MODE_FUSED, MODE_STAGED, BIND_DEVICE_TIMESTAMPS, BIND_TIME_LAUNCHES,  # noqa: F401
                    BIND_ROCTX, BIND_OVERLAP)
+from . import layers as _layers
 from .optim import AdamW, GradNorm
 
 MiB = 1 << 20
@@ -257,6 +258,52 @@ class Reducer:
         if u.shape != (self.R, self.P):
             raise ValueError(f"used flags must have shape ({self.R}, {self.P})")
         self.lib.set_local_used(self.h, np.ascontiguousarray(u, dtype=np.uint8).ravel())
+
+    # -- backward passes that write the bound gradients ------------------------------------
+    def _writable(self, vs, *lists):
+        """Checks a backward pass of the variables vs before it writes anything."""
+        import torch
+        if self._grads is None:
+            raise _abi.DdpbError(_abi.E_STATE, "the reducer is not bound to tensors")
+        if any(len(x) != self.R for x in lists):
+            raise ValueError(f"one tensor for each of the {self.R} replicas is needed")
+        if torch.cuda.current_stream(self.compute_stream.device) != self.compute_stream:
+            raise ValueError("call it on the reducer's compute stream")
+        for v in vs:
+            self.lib.check_writable(self.h, v)
+
+    def layer_norm_backward(self, weight_var: Optional[int], bias_var: Optional[int], dy, h, stats, weight=None,
+                            grad_h=None, drop=None, accumulate: bool = False):
+        """layer_norm_backward for all replicas, the weights' gradients into
+        the bound tensors of variables ``weight_var`` and ``bias_var`` (None for
+        a norm without), which are then marked ready, the bias first. ``dy``,
+        ``h``, ``stats`` and, if given, ``weight``, ``grad_h`` and ``drop`` hold one
+        entry for each replica. ``accumulate``: add to the local steps before.
+        Returns a NormGrads for each replica. On the compute stream, which has
+        to be the current one."""
+        every = lambda x: [None] * self.R if x is None else list(x)  # noqa: E731
+        weight, grad_h, drop = every(weight), every(grad_h), every(drop)
+        vs = [v for v in (bias_var, weight_var) if v is not None]
+        if weight_var is not None and weight_var == bias_var:
+            raise ValueError("weight and bias are two variables")
+        self._writable(vs, dy, h, stats, weight, grad_h, drop)
+        to = lambda r, v: None if v is None else self._grads[r][v]  # noqa: E731
+        out = [_layers.layer_norm_backward(dy[r], h[r], stats[r], weight[r], to(r, weight_var), to(r, bias_var),
+                                           grad_h[r], drop[r], accumulate, lib=self.lib) for r in range(self.R)]
+        self.lib.mark_ready_many(self.h, vs)
+        return out
+
+    def embedding_backward(self, v: int, dy, tokens, scale: float = 1.0, accumulate: bool = False):
+        """embedding_backward for all replicas into the bound tensors of
+        variable v, a table of two dimensions, which is then marked ready. ``dy``
+        and ``tokens`` hold one tensor for each replica; the rest as above."""
+        self._writable([v], dy, tokens)
+        if len(self.shapes[v]) != 2:
+            raise ValueError(f"variable {v} has shape {self.shapes[v]}, not two dimensions")
+        for r in range(self.R):
+            _layers.embedding_backward(dy[r], tokens[r], self._grads[r][v].view(self.shapes[v]), scale, accumulate,
+                                       lib=self.lib)
+        self.lib.mark_ready(self.h, v)
 
     # -- after the synchronisation -------------------------------------------------------
     def _replica_grads(self):

@@ -45,7 +45,7 @@ extern "C" {
 
 typedef struct ddpb_reducer* ddpb_t;
 
-/* element types (DDPB_F16: parameters and gradients of the norm and AdamW only) */
+/* element types (DDPB_F16: not for the reducer's gradients and steps) */
 enum { DDPB_F32 = 0, DDPB_BF16 = 1, DDPB_F16 = 2 };
 
 /* kernel modes for ddpb_bind */
@@ -276,6 +276,12 @@ int ddpb_mark_ready(ddpb_t h, int32_t v);
 /* Same as calling ddpb_mark_ready for vs[0..n-1] in order; stops at the first
  * error and returns it. */
 int ddpb_mark_ready_many(ddpb_t h, const int32_t* vs, int32_t n);
+
+/* Whether a backward pass may write variable v's gradients now, before the hook:
+ * DDPB_OK, or DDPB_E_STATE (not bound; a step set for the coming synchronisation;
+ * a variable that no replica uses in it), DDPB_E_INDEX, DDPB_E_INCOMPLETE (latched
+ * failure), DDPB_E_DOUBLE_READY (marked ready already: its bucket may be reducing). */
+int ddpb_check_writable(ddpb_t h, int32_t v);
 
 /* End of backward: every bucket must have been launched (else
  * DDPB_E_INCOMPLETE, latched; the compute stream is then still made to wait
@@ -517,6 +523,91 @@ int ddpb_adamw_step(ddpb_adamw_t a, ddpb_t h, double lr, const float* lr_device,
  * synchronized. */
 int ddpb_adamw_set_step(ddpb_adamw_t a, int64_t step);
 int ddpb_adamw_get_step(ddpb_adamw_t a, int64_t* step);
+
+/* ---------------------------------------------------------------------------
+ * Beside the matrix products: layer norm, dropout and the embedding, with
+ * their backward passes. The gradients of weights, biases and tables go where
+ * the reducer finds them: into the tensors it is bound to, written or, for
+ * local steps, added to.
+ *
+ * These calls have no handle. Work is enqueued on `stream`, which belongs to
+ * the current device as all addresses do, and nothing waits for it; all memory,
+ * the workspace included, is the caller's, and a workspace serves one call at a
+ * time. Every call may be captured into a graph and replayed.
+ *
+ * Matrices are rows of `cols` consecutive elements. Inputs have a stride, the
+ * elements from one row to the next (>= 0; ignored with one row); outputs are
+ * contiguous. Addresses are aligned to their element type; NULL is allowed
+ * where there are no elements. Outputs overlap neither inputs nor one another,
+ * counting what lies between strided rows (but see ddpb_dropout). Sums and
+ * statistics are held in fp32 and each output is rounded once, to nearest even.
+ * Results are the same bits on every run. Types are DDPB_F32, DDPB_BF16 and
+ * DDPB_F16: `dtype` of activations and their gradients, `weight_dtype` or
+ * `table_dtype` of parameters, `grad_dtype` of their gradients.
+ */
+
+/* Which elements a dropout keeps. With T = p * 65536 rounded to an integer,
+ * element i, counted row by row, is kept where its 16 random bits are >= T, and
+ * then multiplied by 65536 / (65536 - T); else it is 0, whatever stood there.
+ * The bits are half i % 2 (0: the lower) of word i % 8 / 2 of Philox4x32 with 7
+ * rounds of the counter (i / 8, offset + *offset_device), two 64-bit numbers,
+ * lower words first, under the key `seed`. Nothing is stored for the backward
+ * pass, which is the same map of the gradient: pass it the same ddpb_drop. Two
+ * dropouts of one step need offsets (or seeds) of their own. */
+typedef struct ddpb_drop {
+  double p;                       /* in [0, 1] */
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* offset_device;  /* NULL, or a device address that is read when the call
+                                     runs, so that a replayed graph drops anew */
+} ddpb_drop;
+
+/* y = residual + drop(x), without residual if that is NULL. y may be x or
+ * residual itself (contiguous). Rows of more than 2^33 elements must be
+ * contiguous; rows * cols <= 2^40. */
+int ddpb_dropout(int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                 int64_t residual_stride, const ddpb_drop* drop, void* y, void* stream);
+
+/* Layer norm over each row of h = residual + drop(x):
+ *   mean = sum h / cols,  rstd = 1 / sqrt(sum (h - mean)^2 / cols + eps),
+ *   y = (h - mean) rstd weight + bias
+ * residual, drop, weight and bias may be NULL. y comes from h in fp32; `h` (may be
+ * NULL; must be if h is x) is its copy for the backward pass, rounded to dtype.
+ * stats: rows pairs of mean and rstd. rows < 2^31, 1 <= cols <= 2^20. */
+int ddpb_layer_norm(int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                    int64_t residual_stride, const ddpb_drop* drop, const void* weight, const void* bias,
+                    int32_t weight_dtype, double eps, void* y, void* h, float* stats, void* stream);
+
+/* Its gradients, with n = (h - mean) rstd and g = dy weight:
+ *   dh = rstd (g - mean of g - n mean of (g n)) + grad_h     (residual's gradient)
+ *   dx = drop(dh)                                            (x's gradient)
+ *   dweight = sum over rows of dy n,  dbias = sum over rows of dy
+ * grad_h (may be NULL): a gradient that reaches h from elsewhere. dx is given if
+ * drop has p > 0 (2^-17 or more), else NULL: dh is x's gradient too. dweight, dbias: NULL if not
+ * wanted; with `accumulate` they are added to. The workspace is needed for those
+ * two only (256-byte aligned). */
+int ddpb_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int64_t* bytes);
+int ddpb_layer_norm_backward(int64_t rows, int64_t cols, int32_t dtype, const void* dy, int64_t dy_stride,
+                             const void* h, int64_t h_stride, const float* stats, const void* grad_h,
+                             int64_t grad_h_stride, const ddpb_drop* drop, const void* weight, int32_t weight_dtype,
+                             void* dh, void* dx, void* dweight, void* dbias, int32_t grad_dtype, int32_t accumulate,
+                             void* workspace, int64_t ws_bytes, void* stream);
+
+/* y_i = scale * table[tokens[i]] + residual_i for n tokens of 4 or 8 bytes
+ * (int32_t, int64_t); residual may be NULL. A token outside of 0 .. vocab - 1
+ * stands for a row of zeros and takes no gradient (padding; the other parts of a
+ * table that is split by rows). n <= 2^30, vocab <= 2^31 - 2, 1 <= cols <= 2^24. */
+int ddpb_embedding(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols, const void* table,
+                   int32_t table_dtype, double scale, const void* residual, int64_t residual_stride, void* y,
+                   int32_t dtype, void* stream);
+
+/* dtable[v] = scale * sum of dy_i over the places i with tokens[i] = v, the whole
+ * table (rows of no token become 0); with `accumulate` the sums are added to what
+ * stands there and other rows are left alone. The workspace is 256-byte aligned. */
+int ddpb_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t cols, int64_t* bytes);
+int ddpb_embedding_backward(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols,
+                            const void* dy, int64_t dy_stride, int32_t dtype, double scale, void* dtable,
+                            int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics.

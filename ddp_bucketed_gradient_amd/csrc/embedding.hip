@@ -66,9 +66,9 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(Lookup a) {
 // The gradient: dtable[v] = scale * sum of dy_i over the places i of token v, in
 // order of i and without atomics on values, so the same bits on every run.
 //
-//  1. Sort the places by token: a stable radix sort, `digit` bits a pass. With
-//     one tile of keys one workgroup does it in LDS; with more each pass is a
-//     histogram of every tile and a scatter. Beside it, workgroups that would
+//  1. Sort the places by token, stably: a radix sort, `digit` bits a pass, each
+//     a histogram of every tile of keys and a scatter; few tokens in one launch,
+//     by ranges of them. Beside it, workgroups that would
 //     be idle write the zeros of a gradient that is not added to.
 //  2. Sum: the sorted places are cut into units of equal length, so that a
 //     token that holds many places (padding, the commonest words) is shared
@@ -82,14 +82,21 @@ struct Zeros {
   uint64_t head, tail;   // odd bytes before and behind the pieces: addresses
   int32_t head_bytes, tail_bytes;   // 0 but in the first launch
 };
-constexpr int64_t kZeroPieces = kSortThreads * 8;   // of a workgroup
+constexpr int kZeroBlocks = 448;                    // workgroups that write them, at most
+constexpr int64_t kZeroPieces = kSortThreads * 8;   // that one of them writes at a time
 
-__device__ __forceinline__ void write_zeros(const Zeros& z, int64_t block) {
-  const int64_t from = z.first + block * kZeroPieces;
+// Non-temporal stores of device scope: BERT-large's 125 MB of zeros beside the
+// sort take 26 us instead of 36, and the sum that follows, whose reads would meet
+// the caches full of them, 12.5 us instead of 22.6.
+__device__ __forceinline__ void write_zeros(const Zeros& z, uint32_t block, uint32_t blocks) {
+  for (int64_t from = z.first + block * kZeroPieces; from < z.last; from += blocks * kZeroPieces) {
+    const uint64_t base = z.at + static_cast<uint64_t>(from) * 16;
+    const int64_t rest = min((z.last - from) * 16, kZeroPieces * 16);
+    const auto r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, static_cast<int>(rest), 0x00020000);
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int64_t i = from + u * kSortThreads + threadIdx.x;
-    if (i < z.last) G<v4u>(z.at)[i] = v4u{0, 0, 0, 0};
+    for (int u = 0; u < 8; ++u)
+      __builtin_amdgcn_raw_buffer_store_b128(v4u{0, 0, 0, 0}, r, (u * kSortThreads + threadIdx.x) * 16, 0, kPolicyDeviceNT);
+
   }
   if (block == 0) {   // element by element (of at least two bytes)
     if (static_cast<int>(threadIdx.x) * 2 < z.head_bytes) G<uint16_t>(z.head)[threadIdx.x] = 0;
@@ -137,6 +144,19 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// The lanes that are there and hold the same digit.
+template <int BITS>
+__device__ __forceinline__ uint64_t equal_digits(uint32_t d, bool there) {
+  uint64_t same = __ballot(there);
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
+    const bool one = d >> b & 1;
+    const uint64_t ones = __ballot(one);
+    same &= one ? ones : ~ones;
+  }
+  return same;
+}
+
 // Each key's place among the equal digits of its wave, and the waves' counts.
 // Stable: the keys of a wave are taken 64 at a time in their order, and a key's
 // rank is the count of equal digits in the lanes below it.
@@ -182,61 +202,138 @@ __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* waves) {
   return before + sum - x;
 }
 
-// All passes for one tile of keys, in LDS.
-__global__ __launch_bounds__(kSortThreads) void sort_tile_kernel(Sort a) {
-  if (blockIdx.x != 0) {
-    write_zeros(a.zeros, static_cast<int64_t>(blockIdx.x) - 1);
+// All of the sort in one launch, for up to kRangeKeys tokens. Workgroup g of
+// kRanges takes the tokens t with t % kRanges = g (so that neighbouring common
+// ones do not meet in one), finds them among all, and sorts them by t / kRanges
+// in LDS, six bits a pass, one counter of a wave's digits to a thread. What it
+// counts of the ranges before its own is where its places begin. The order is
+// one of groups: t % kRanges, then t.
+constexpr int kRangeBits = 6;
+struct RangeLds {
+  uint32_t keys[kRangeKeys];
+  uint16_t places[kRangeKeys];
+  uint16_t count[kWaves << kRangeBits];     // [digit][wave]
+  uint32_t waves[kWaves];
+  uint2 here[kWaves];                       // of each wave: tokens of the range, and of those before it
+};
+
+// Collects a range's tokens, in their order, E of all tokens to a lane; returns
+// where the range's places begin and how many there are.
+template <int E>
+__device__ __forceinline__ uint2 collect(const Sort& a, RangeLds& s) {
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, range = blockIdx.x;
+  const uint32_t n = static_cast<uint32_t>(a.n), each = (n + kSortThreads - 1) / kSortThreads;
+  const uint32_t at = wave * 64 * each + lane;     // a wave's share is consecutive: 64 * each
+  uint32_t key[E], total = 0, below = 0;
+  auto read = [&](auto token) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      key[e] = a.vocab;
+      if (e < static_cast<int>(each) && at + e * 64 < n) {
+        const auto t = G<const decltype(token)>(a.tokens)[at + e * 64];
+        key[e] = t < a.vocab ? static_cast<uint32_t>(t) : a.vocab;
+      }
+    }
+  };
+  if (a.token_bytes == 4) read(uint32_t());
+  else read(uint64_t());
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    total += __popcll(__ballot(key[e] < a.vocab && key[e] % kRanges == range));
+    below += __popcll(__ballot(key[e] < a.vocab && key[e] % kRanges < range));
+  }
+  if (lane == 0) s.here[wave] = make_uint2(total, below);
+  __syncthreads();
+  uint32_t to = 0, m = 0, first = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < static_cast<uint32_t>(kWaves); ++w) {
+    if (w < wave) to += s.here[w].x;
+    m += s.here[w].x;
+    first += s.here[w].y;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const bool in = key[e] < a.vocab && key[e] % kRanges == range;
+    const uint64_t all = __ballot(in);
+    if (in) {
+      const uint32_t i = to + __popcll(all & ((uint64_t(1) << lane) - 1));
+      s.keys[i] = key[e] / kRanges;
+      s.places[i] = static_cast<uint16_t>(at + e * 64);
+    }
+    to += __popcll(all);
+  }
+  return make_uint2(first, m);
+}
+
+// One pass over the m keys of a range, M of them to a lane.
+template <int M>
+__device__ __forceinline__ void sort_range(const Sort& a, RangeLds& s, uint32_t first, uint32_t m, int shift, bool final) {
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, mine = (m + kSortThreads - 1) / kSortThreads;
+  const uint32_t at = wave * 64 * mine + lane;
+  uint32_t key[M], place[M], rank[M];
+  s.count[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < M; ++e) {
+    const bool there = e < static_cast<int>(mine) && at + e * 64 < m;
+    key[e] = place[e] = rank[e] = 0;
+    if (there) {
+      key[e] = s.keys[at + e * 64];
+      place[e] = s.places[at + e * 64];
+    }
+    const uint32_t d = key[e] >> shift & ((1u << kRangeBits) - 1);
+    const uint64_t same = equal_digits<kRangeBits>(d, there), lower = same & ((uint64_t(1) << lane) - 1);
+    if (there) {
+      const uint32_t before = s.count[d * kWaves + wave];
+      rank[e] = before + __popcll(lower);
+      wave_fence();
+      if (lower == 0) s.count[d * kWaves + wave] = static_cast<uint16_t>(before + __popcll(same));
+    }
+    wave_fence();
+  }
+  __syncthreads();
+  const uint32_t before = scan(s.count[threadIdx.x], s.waves);
+  s.count[threadIdx.x] = static_cast<uint16_t>(before);
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < M; ++e) {
+    if (e >= static_cast<int>(mine) || at + e * 64 >= m) continue;
+    const uint32_t to = s.count[(key[e] >> shift & ((1u << kRangeBits) - 1)) * kWaves + wave] + rank[e];
+    if (final) {
+      a.keys[first + to] = key[e] * kRanges + blockIdx.x;
+      a.order[first + to] = place[e];
+    } else {
+      s.keys[to] = key[e];
+      s.places[to] = static_cast<uint16_t>(place[e]);
+    }
+  }
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_ranges_kernel(Sort a) {
+  extern __shared__ char raw_lds[];
+  if (blockIdx.x >= kRanges) {
+    write_zeros(a.zeros, blockIdx.x - kRanges, gridDim.x - kRanges);
     return;
   }
-  __shared__ uint16_t count[kWaves][kBins];
-  __shared__ uint32_t keys[kSortTile], base[kBins], waves[kWaves];
-  __shared__ uint16_t places[kSortTile];
-  if (threadIdx.x == 0) *a.joins = 0;
-  uint32_t key[kSortKeys], place[kSortKeys], rank[kSortKeys];
-  load_keys(a, 0, key, place);
-  const uint32_t at = (threadIdx.x >> 6) * (64 * kSortKeys) + (threadIdx.x & 63);
-  for (int pass = 0, shift = 0; pass < a.passes; ++pass, shift += a.digit) {
-    rank_keys(key, rank, at, a.n, shift, a.digit, count);
-    __syncthreads();
-    uint32_t all = 0;
-    const uint32_t bins = 1u << a.digit;
-    if (threadIdx.x < bins) {
-      for (int w = 0; w < kWaves; ++w) {
-        const uint32_t x = count[w][threadIdx.x];
-        count[w][threadIdx.x] = static_cast<uint16_t>(all);
-        all += x;
-      }
-    }
-    const uint32_t before = scan(all, waves);
-    if (threadIdx.x < bins) base[threadIdx.x] = before;
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kSortKeys; ++e) {
-      if (at + e * 64 >= a.n) continue;
-      const uint32_t d = key[e] >> shift & (bins - 1), to = base[d] + count[threadIdx.x >> 6][d] + rank[e];
-      if (pass == a.passes - 1) {
-        a.keys[to] = key[e];
-        a.order[to] = place[e];
-      } else {
-        keys[to] = key[e];
-        places[to] = static_cast<uint16_t>(place[e]);
-      }
-    }
-    __syncthreads();
-    if (pass < a.passes - 1) {
-#pragma unroll
-      for (int e = 0; e < kSortKeys; ++e) {
-        if (at + e * 64 >= a.n) continue;
-        key[e] = keys[at + e * 64];
-        place[e] = places[at + e * 64];
-      }
-    }
+  RangeLds& s = *reinterpret_cast<RangeLds*>(raw_lds);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.joins = 0;
+  const uint2 got = a.n <= 4 * kSortThreads ? collect<4>(a, s) : collect<kRangeKeys / kSortThreads>(a, s);
+  const uint32_t first = got.x, m = got.y;
+  // behind the last range: the tokens outside of the table
+  if (blockIdx.x == kRanges - 1)
+    for (uint32_t i = first + m + threadIdx.x; i < a.n; i += kSortThreads) a.keys[i] = a.vocab;
+  __syncthreads();
+  for (int pass = 0; pass < a.passes; ++pass) {
+    // few keys, but where one token holds most places: the code of sixteen is long
+    if (m <= kSortThreads) sort_range<1>(a, s, first, m, pass * kRangeBits, pass == a.passes - 1);
+    else sort_range<kRangeKeys / kSortThreads>(a, s, first, m, pass * kRangeBits, pass == a.passes - 1);
   }
 }
 
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(Sort a) {
   if (blockIdx.x >= a.tiles) {
-    write_zeros(a.zeros, static_cast<int64_t>(blockIdx.x) - a.tiles);
+    write_zeros(a.zeros, blockIdx.x - a.tiles, gridDim.x - a.tiles);
     return;
   }
   __shared__ uint32_t count[kBins];
@@ -282,7 +379,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(Sort a) {
 
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(Sort a) {
   if (blockIdx.x >= a.tiles) {
-    write_zeros(a.zeros, static_cast<int64_t>(blockIdx.x) - a.tiles);
+    write_zeros(a.zeros, blockIdx.x - a.tiles, gridDim.x - a.tiles);
     return;
   }
   __shared__ uint16_t count[kWaves][kBins];
@@ -326,144 +423,163 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(Sort a) {
   }
 }
 
+// A wave sums eight columns a lane of one unit. The keys and places of 64 sorted
+// places lie in its lanes, so that the run ends are a mask and everything but
+// the rows themselves is uniform. The rows of kAhead places are loaded together,
+// with what stands in the table where the sums are added to that.
 struct Sum {
-  uint64_t dy, dtable;
-  int64_t dy_stride, n, unit, units;
-  const uint32_t *keys, *order;
+  uint64_t dy, dtable, keys, order;
+  uint64_t dy_row, table_row;   // bytes from row to row
+  uint32_t n, unit, units;      // at most 2^30 places
+  uint32_t cols, vocab;
   float* partials;              // [unit][run from the left, run to the right][cols]
   uint32_t *joins, *list;
-  uint32_t cols, vocab;
-  int32_t grad_dtype, accumulate;
   float scale;
 };
 
-__device__ __forceinline__ void write_row(const Sum& a, uint32_t token, uint32_t c, int64_t left, v8f x) {
-  const uint64_t at = a.dtable + (static_cast<uint64_t>(token) * a.cols + c) * (a.grad_dtype == kF32 ? 4 : 2);
-  x = x * a.scale;
-  if (a.accumulate) x = x + load8(a.grad_dtype, at, left);
-  store8(a.grad_dtype, at, left, x);
+// Written before this kernel, by one that has ended: a scalar load.
+__device__ __forceinline__ uint32_t key_at(const Sum& a, uint32_t i) {
+  return *(const __attribute__((address_space(4))) uint32_t*)(a.keys + static_cast<uint64_t>(i * 4));
 }
 
-// A unit has LANES lanes, eight columns each.
-constexpr int kAhead = 8;       // places whose rows are loaded together
-template <int D>
-__global__ __launch_bounds__(256) void sum_kernel(Sum a, int lanes) {
+__device__ __forceinline__ uint32_t lane_of(uint32_t x, int i) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), i));
+}
+
+// A wave sums eight columns a lane of one unit. The keys and places of 64 sorted
+// places lie in its lanes, so that the run ends are a mask and everything but
+// the rows themselves is uniform. The rows of kAhead places are loaded together,
+// with what stands in the table where the sums are added to that. TAIL: rows
+// that do not end on a multiple of eight. The code of each variant is kept short
+// (one wave runs most of it once): with the tails and 64-bit indexes in one
+// kernel of 11 KB half of the waves' time went into fetching it.
+template <int D, int GD, bool ADD, bool TAIL>
+__global__ __launch_bounds__(256) void sum_kernel(Sum a) {
   typedef typename Of<D>::one one;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
+  typedef typename Of<GD>::one grad_one;
+  constexpr int kAhead = ADD ? 4 : 8;
+  const uint32_t u = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (u >= a.units) return;
-  const uint32_t c = (blockIdx.y * lanes + threadIdx.x % lanes) * 8;
-  const int64_t left = static_cast<int64_t>(a.cols) - c;
-  if (left <= 0) return;
-  const int64_t s = u * a.unit, e = min(s + a.unit, a.n);
-  const uint32_t first = a.keys[s], last = a.keys[e - 1];
+  const uint32_t lane = threadIdx.x & 63, c = blockIdx.y * 512 + lane * 8;
+  const int left = c >= a.cols ? 0 : TAIL ? static_cast<int>(min(a.cols - c, 8u)) : 8;
+  const uint32_t s = u * a.unit, e = min(s + a.unit, a.n), e2 = min(e + a.unit, a.n);
+  const uint32_t first = key_at(a, s), last = key_at(a, e - 1);
+  const uint32_t before = key_at(a, s > 0 ? s - 1 : 0), unit_before = key_at(a, s > 0 ? s - a.unit : 0);
+  const uint32_t behind = key_at(a, e < a.n ? e : e - 1), unit_behind = key_at(a, e2 - 1);
   if (first >= a.vocab) return;
   // the run that comes in from the left: another unit's, unless it covers a whole unit
-  const bool from_left = s > 0 && a.keys[s - 1] == first;
-  const bool mine = !from_left || last == first || a.keys[s - a.unit] == first;
+  const bool from_left = s > 0 && before == first;
+  const bool mine = !from_left || last == first || unit_before == first;
   // the run that goes out to the right: ours to its end, unless it covers a whole unit
-  const bool to_right = e < a.n && last < a.vocab && a.keys[e] == last;
-  const int64_t e2 = min(e + a.unit, a.n);
-  const bool long_right = to_right && (first == last || a.keys[e2 - 1] == last);
-  const int64_t stop = to_right && !long_right ? e2 : e;
-  float* const partial = a.partials + u * 2 * a.cols + c;
-  auto put = [&](float* p, v8f x) { store8<kF32>(reinterpret_cast<uint64_t>(p), left, x); };
+  const bool to_right = e < a.n && last < a.vocab && behind == last;
+  const bool long_right = to_right && (first == last || unit_behind == last);
+  const uint32_t stop = to_right && !long_right ? e2 : e;
+  const uint64_t partial = reinterpret_cast<uint64_t>(a.partials) + (static_cast<uint64_t>(u) * 2 * a.cols + c) * 4;
 
-  uint32_t run = first;
-  bool open_left = from_left;     // the run in `x` began in another unit
   v8f x = 0.0f;
-  for (int64_t j = s; j < stop; j += kAhead) {
-    uint32_t key[kAhead];
-    v8f d[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      key[i] = j + i < stop ? a.keys[j + i] : a.vocab;
-      if (j + i >= e && key[i] != last) key[i] = a.vocab;        // behind the run that we finish
-      d[i] = 0.0f;
-      if (key[i] < a.vocab && (mine || key[i] != first))
-        d[i] = load8<D>(a.dy + (a.order[j + i] * a.dy_stride + c) * sizeof(one), left);
+  bool open_left = from_left && mine, pending = false;   // the run in x began in another unit; it has not ended
+  for (uint32_t p = s; p < stop; p += 64) {
+    const uint32_t i = p + lane;
+    uint32_t key = a.vocab, next = a.vocab, place = 0;
+    if (i < stop) {
+      key = *G<const uint32_t>(a.keys + static_cast<uint64_t>(i * 4));
+      place = *G<const uint32_t>(a.order + static_cast<uint64_t>(i * 4));
+      if (i + 1 < a.n) next = *G<const uint32_t>(a.keys + static_cast<uint64_t>(i * 4 + 4));
     }
+    const bool ours = key < a.vocab && (mine || key != first) && (i < e || key == last);
+    const uint64_t todo = __ballot(ours), ends = __ballot(ours && key != next);
+    if (todo == 0) continue;
+    const int from = __builtin_ctzll(todo), to = 64 - __builtin_clzll(todo);    // they are consecutive
+    for (int j = from; j < to; j += kAhead) {
+      Raw<D> rows[kAhead];
+      Raw<GD> old[ADD ? kAhead : 1];
+      if (left > 0) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (key[i] != run) {
-        if (run < a.vocab) {
-          if (!open_left) write_row(a, run, c, left, x);
-          else if (mine) put(partial, x);
+        for (int k = 0; k < kAhead; ++k) {
+          const int at = min(j + k, to - 1);
+          rows[k] = load_raw<D, TAIL>(a.dy + lane_of(place, at) * a.dy_row + c * static_cast<uint32_t>(sizeof(one)), left);
+          if constexpr (ADD) {
+            if (j + k < to && (ends >> at & 1))
+              old[k] = load_raw<GD, TAIL>(a.dtable + lane_of(key, at) * a.table_row + c * static_cast<uint32_t>(sizeof(grad_one)), left);
+          }
         }
-        run = key[i];
-        open_left = false;
-        x = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (j + k >= to) break;
+          x = x + widen<D>(rows[k]);
+          if ((ends >> (j + k) & 1) == 0) continue;
+          if (open_left) {
+            store8<kF32, TAIL>(partial, left, x);
+          } else {
+            x = x * a.scale;
+            if constexpr (ADD) x = x + widen<GD>(old[k]);
+            store8<GD, TAIL>(a.dtable + lane_of(key, j + k) * a.table_row + c * static_cast<uint32_t>(sizeof(grad_one)), left, x);
+          }
+          open_left = false;
+          x = 0.0f;
+        }
       }
-      x = x + d[i];
     }
+    pending = (ends >> (to - 1) & 1) == 0;
+    open_left = open_left && ends == 0;               // the same in lanes without columns
   }
-  if (run >= a.vocab) return;
-  if (open_left) {
-    if (mine) put(partial, x);
-  } else if (!long_right) {
-    write_row(a, run, c, left, x);
-  } else {
-    put(partial + a.cols, x);
-    if (c == 0) a.list[atomicAdd(a.joins, 1u)] = static_cast<uint32_t>(u);
-  }
+  if (!pending) return;
+  if (left > 0) store8<kF32, TAIL>(partial + (open_left ? 0 : static_cast<uint64_t>(a.cols) * 4), left, x);
+  if (!open_left && c == 0) a.list[atomicAdd(a.joins, 1u)] = u;
 }
 
-// The runs that cover whole units: 64 columns to a workgroup, in which 16 lanes
-// side by side hold four columns each and 16 rows of lanes take every 16th unit.
-constexpr int kJoinCols = 64;
+// The runs that cover whole units: 16 columns to a wave, four to a lane, and 16
+// lanes for each of them, which take every 16th unit.
+constexpr int kJoinCols = 16, kJoinLanes = kJoinCols / 4, kJoinLines = 64 / kJoinLanes, kJoinAhead = 4;
+template <int GD, bool ADD>
 __global__ __launch_bounds__(256) void join_kernel(Sum a) {
-  __shared__ v4f part[16][16];
-  __shared__ uint32_t found;
-  const uint32_t slices = (a.cols + kJoinCols - 1) / kJoinCols;
-  const uint64_t work = static_cast<uint64_t>(*a.joins) * slices;
-  const uint32_t lane = threadIdx.x & 15, line = threadIdx.x >> 4;
-  for (uint64_t k = blockIdx.x; k < work; k += gridDim.x) {
-    const int64_t u = a.list[k / slices];
-    const uint32_t c = static_cast<uint32_t>(k % slices) * kJoinCols + lane * 4;
-    const uint32_t token = a.keys[(u + 1) * a.unit - 1];
-    // units behind u that begin with the token
-    int64_t count = 0;
-    for (bool more = true; more; count += found, more = found == 256) {
-      const int64_t next = u + 1 + count + threadIdx.x;
-      __syncthreads();
-      if (threadIdx.x == 0) found = 0;
-      __syncthreads();
-      const bool same = next < a.units && a.keys[next * a.unit] == token;
-      const uint64_t votes = __ballot(same);
-      if ((threadIdx.x & 63) == 0) atomicAdd(&found, static_cast<uint32_t>(__popcll(votes)));
-      __syncthreads();
-    }
-    const uint32_t left = c < a.cols ? min(a.cols - c, 4u) : 0;
+  typedef typename Of<GD>::one one;
+  typedef v4f any __attribute__((aligned(4)));
+  const uint32_t lane = threadIdx.x % kJoinLanes, line = (threadIdx.x & 63) / kJoinLanes, joins = *a.joins;
+  const uint32_t c = (blockIdx.y * 4 + (threadIdx.x >> 6)) * kJoinCols + lane * 4;
+  const uint32_t left = c < a.cols ? min(a.cols - c, 4u) : 0;
+  for (uint32_t k = blockIdx.x; k < joins; k += gridDim.x) {
+    const uint32_t u = a.list[k];
+    const uint32_t token = *G<const uint32_t>(a.keys + static_cast<uint64_t>(((u + 1) * a.unit - 1) * 4));
     v4f x = 0.0f;
-    // part 0 is the beginning in unit u, part i the run in unit u + i
-#pragma unroll 4
-    for (int64_t i = line; i <= count; i += 16) {
-      const float* p = a.partials + ((u + i) * 2 + (i == 0)) * a.cols + c;
-      v4f y = 0.0f;
+    // part 0 is the beginning in unit u, part i what unit u + i begins with, as long as that is the token
+    bool more = left > 0;
+    for (uint32_t i = line; __any(more); i += kJoinLines * kJoinAhead) {
+      bool same[kJoinAhead];
+      v4f y[kJoinAhead];
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j)
-        if (j < left) y[j] = p[j];
-      x = x + y;
-    }
-    part[line][lane] = x;
-    __syncthreads();
-    if (line == 0) {
-      for (int l = 1; l < 16; ++l) x = x + part[l][lane];
-      const int size = a.grad_dtype == kF32 ? 4 : 2;
-      const uint64_t at = a.dtable + (static_cast<uint64_t>(token) * a.cols + c) * size;
-#pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) {
-        if (j >= left) continue;
-        auto put = [&](auto one) {
-          auto* p = G<decltype(one)>(at) + j;
-          const float old = a.accumulate ? static_cast<float>(*p) : 0.0f;
-          *p = static_cast<decltype(one)>(x[j] * a.scale + old);
-        };
-        if (a.grad_dtype == kF32) put(float());
-        else if (a.grad_dtype == kBF16) put(__bf16());
-        else put(_Float16());
+      for (int q = 0; q < kJoinAhead; ++q) {
+        const uint32_t at = u + i + q * kJoinLines;
+        same[q] = more && at < a.units && (at == u || *G<const uint32_t>(a.keys + static_cast<uint64_t>(at * a.unit * 4)) == token);
       }
+#pragma unroll
+      for (int q = 0; q < kJoinAhead; ++q) {
+        const uint32_t at = u + i + q * kJoinLines;
+        y[q] = 0.0f;
+        if (!same[q]) continue;
+        const float* p = a.partials + (static_cast<uint64_t>(at) * 2 + (at == u)) * a.cols + c;
+        if (left == 4) {
+          y[q] = *reinterpret_cast<const any*>(p);
+        } else {
+#pragma unroll
+          for (uint32_t j = 0; j < 3; ++j)
+            if (j < left) y[q][j] = p[j];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kJoinAhead; ++q) x = x + y[q];
+      more = same[kJoinAhead - 1];
     }
-    __syncthreads();
+#pragma unroll
+    for (int d = kJoinLanes; d < 64; d *= 2) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] += __shfl_xor(x[j], d, 64);
+    }
+    if (line != 0) continue;
+    auto* p = G<one>(a.dtable + token * a.table_row + c * static_cast<uint32_t>(sizeof(one)));
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+      if (j < left) p[j] = static_cast<one>(x[j] * a.scale + (ADD ? static_cast<float>(p[j]) : 0.0f));
   }
 }
 
@@ -501,10 +617,10 @@ Zeros zeros_of(const LookupBackwardArgs& a, int i, int launches) {
   return z;
 }
 
-// Workgroups for a share of the zeros; threads of a launch stay below 2^32.
+// Workgroups for a share of the zeros.
 int64_t zero_blocks(const Zeros& z) {
   const int64_t b = (z.last - z.first + kZeroPieces - 1) / kZeroPieces;
-  return b == 0 && z.head_bytes + z.tail_bytes > 0 ? 1 : b;
+  return b == 0 && z.head_bytes + z.tail_bytes > 0 ? 1 : b < kZeroBlocks ? b : kZeroBlocks;
 }
 
 }  // namespace
@@ -544,14 +660,14 @@ int enqueue_lookup_backward(const LookupBackwardArgs& a, std::string* err) {
   k.totals = words(p.totals);
   k.joins = words(p.joins);
   int sorted = 0;                                  // which of the two buffers holds the result
-  if (p.tiles == 1) {
+  if (p.tiles == 0) {
     k.tokens = addr(a.tokens);
     k.keys = words(p.keys[0]);
     k.order = words(p.order[0]);
     k.zeros = zeros_of(a, 0, 1);
-    hipLaunchKernelGGL(sort_tile_kernel, dim3(static_cast<unsigned>(1 + zero_blocks(k.zeros))), dim3(kSortThreads), 0,
-                       s, k);
-    HIP_OK(hipGetLastError(), "launch sort_tile_kernel");
+    hipLaunchKernelGGL(sort_ranges_kernel, dim3(static_cast<unsigned>(kRanges + zero_blocks(k.zeros))),
+                       dim3(kSortThreads), sizeof(RangeLds), s, k);
+    HIP_OK(hipGetLastError(), "launch sort_ranges_kernel");
   } else {
     k.scanned = p.tiles > kScanTiles;
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -577,21 +693,29 @@ int enqueue_lookup_backward(const LookupBackwardArgs& a, std::string* err) {
     }
   }
   if (a.n == 0) return kOk;
-  const Sum m = {addr(a.dy.data), addr(a.dtable), a.dy.stride, a.n, p.unit, p.units, words(p.keys[sorted]),
-                 words(p.order[sorted]), reinterpret_cast<float*>(ws + p.partials), words(p.joins), words(p.list),
-                 static_cast<uint32_t>(a.cols), static_cast<uint32_t>(a.vocab), a.grad_dtype, a.accumulate ? 1 : 0,
-                 a.scale};
-  const int64_t groups = (a.cols + kGroup - 1) / kGroup;
-  int lanes = 8;
-  while (lanes < 256 && lanes < groups) lanes *= 2;
-  const int64_t each = 256 / lanes;
-  const dim3 grid(static_cast<unsigned>((p.units + each - 1) / each), static_cast<unsigned>((groups + lanes - 1) / lanes));
-  by_type(a.dtype, [&](auto d) { hipLaunchKernelGGL((sum_kernel<decltype(d)::value>), grid, dim3(256), 0, s, m, lanes); });
-  HIP_OK(hipGetLastError(), "launch sum_kernel");
-  if (p.units > 1) {
-    hipLaunchKernelGGL(join_kernel, dim3(1024), dim3(256), 0, s, m);
-    HIP_OK(hipGetLastError(), "launch join_kernel");
-  }
+  const Sum m = {addr(a.dy.data), addr(a.dtable), addr(words(p.keys[sorted])), addr(words(p.order[sorted])),
+                 static_cast<uint64_t>(a.dy.stride * dtype_size(a.dtype)),
+                 static_cast<uint64_t>(a.cols * dtype_size(a.grad_dtype)), static_cast<uint32_t>(a.n),
+                 static_cast<uint32_t>(p.unit), static_cast<uint32_t>(p.units), static_cast<uint32_t>(a.cols),
+                 static_cast<uint32_t>(a.vocab), reinterpret_cast<float*>(ws + p.partials), words(p.joins),
+                 words(p.list), a.scale};
+  const dim3 grid(static_cast<unsigned>((p.units + 3) / 4), static_cast<unsigned>((a.cols + 511) / 512));
+  const int64_t slices = (a.cols + 4 * kJoinCols - 1) / (4 * kJoinCols), runs = slices < 32 ? 2048 / slices : 64;
+  const dim3 join_grid(static_cast<unsigned>(runs < p.units ? runs : p.units), static_cast<unsigned>(slices));
+  const bool tail = a.cols % 8 != 0;
+  by_type(a.grad_dtype, [&](auto g) {
+    constexpr int GD = decltype(g)::value;
+    by_type(a.dtype, [&](auto d) {
+      constexpr int TD = decltype(d)::value;
+      auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, m); };
+      if (a.accumulate) tail ? go(sum_kernel<TD, GD, true, true>) : go(sum_kernel<TD, GD, true, false>);
+      else tail ? go(sum_kernel<TD, GD, false, true>) : go(sum_kernel<TD, GD, false, false>);
+    });
+    if (p.units <= 1) return;
+    if (a.accumulate) hipLaunchKernelGGL((join_kernel<GD, true>), join_grid, dim3(256), 0, s, m);
+    else hipLaunchKernelGGL((join_kernel<GD, false>), join_grid, dim3(256), 0, s, m);
+  });
+  HIP_OK(hipGetLastError(), "launch sum_kernel or join_kernel");
   return kOk;
 }
 

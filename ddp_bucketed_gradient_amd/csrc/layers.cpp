@@ -77,20 +77,16 @@ NormShape norm_shape(int64_t cols) {
   if (cols <= 128 * kGroup) return {64, 2};
   if (cols <= 256 * kGroup) return {256, 1};
   if (cols <= 512 * kGroup) return {256, 2};
-  if (cols <= 1024 * kGroup) return {1024, 1};
+  if (cols <= 1024 * kGroup) return {512, 2};
   if (cols <= 2048 * kGroup) return {1024, 2};
   return {0, 0};
 }
 
-int norm_backward_threads(NormShape s) {
-  return s.lanes == 0 || s.lanes == 1024 ? 1024 : s.lanes == 256 ? 256 : 512;
-}
-
 int32_t norm_backward_blocks(int64_t rows, int64_t cols) {
   const NormShape s = norm_shape(cols);
-  const int threads = norm_backward_threads(s);
-  const int64_t at_once = s.lanes == 0 ? 1 : threads / s.lanes;       // rows of a workgroup
-  int64_t most = threads == 1024 ? 512 : threads == 512 ? 512 : 1024;
+  // rows of a workgroup at once, and workgroups that leave a partial sum: eight waves a CU
+  const int64_t at_once = s.lanes == 0 || s.lanes > 64 ? 1 : 512 / s.lanes;
+  int64_t most = s.lanes == 256 ? 512 : 256;
   if (s.lanes == 0) most = std::max<int64_t>(32, std::min<int64_t>(256, (int64_t(64) << 20) / (8 * cols)));
   return static_cast<int32_t>(std::max<int64_t>(1, std::min(most, (rows + at_once - 1) / at_once)));
 }
@@ -202,15 +198,20 @@ LookupPlan lookup_plan(int64_t n, int64_t vocab, int64_t cols) {
   LookupPlan p{};
   int bits = 1;                                      // a token is 0..vocab, vocab standing for all others
   while ((int64_t(1) << bits) <= vocab) ++bits;
-  p.passes = (bits + kMaxDigit - 1) / kMaxDigit;
-  p.digit = (bits + p.passes - 1) / p.passes;
-  p.tiles = std::max<int64_t>(1, (n + kSortTile - 1) / kSortTile);
-  // Units small enough that about 2048 waves share the sum (eight a CU), at least
-  // 8 places each, and at most 4096 units, which bounds the partial sums.
+  if (n <= kRangeKeys) {                             // t / kRanges, six bits a pass
+    p.passes = (std::max(bits - 5, 1) + 5) / 6;
+    p.digit = 6;
+  } else {
+    p.passes = (bits + kMaxDigit - 1) / kMaxDigit;
+    p.digit = (bits + p.passes - 1) / p.passes;
+    p.tiles = (n + kSortTile - 1) / kSortTile;
+  }
+  // Units of 8 places or more, so that up to 4096 waves (16 a CU) share the sum; at
+  // most 65536 units, which bounds the partial sums.
   const int64_t waves = (cols + 64 * kGroup - 1) / (64 * kGroup);
   p.unit = 8;
-  while (p.unit < 64 && n * waves > p.unit * 2048) p.unit *= 2;
-  while (n > p.unit * 4096) p.unit *= 2;
+  while (p.unit < 128 && n * waves > p.unit * 4096) p.unit *= 2;
+  while (n > p.unit * 65536) p.unit *= 2;
   p.units = (n + p.unit - 1) / p.unit;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -222,7 +223,7 @@ LookupPlan lookup_plan(int64_t n, int64_t vocab, int64_t cols) {
     p.keys[i] = take(n * 4);
     p.order[i] = take(n * 4);
   }
-  p.hist = take(p.tiles > 1 ? (p.tiles << p.digit) * 4 : 0);
+  p.hist = take((p.tiles << p.digit) * 4);
   p.totals = take(int64_t(4) << p.digit);
   p.joins = take(4);
   p.list = take(p.units * 4);

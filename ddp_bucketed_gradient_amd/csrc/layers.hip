@@ -64,24 +64,52 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float* lds) {
 __device__ __forceinline__ float total(v8f x) { return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])); }
 __device__ __forceinline__ v8f fma8(v8f a, v8f b, v8f c) { return __builtin_elementwise_fma(a, b, c); }
 
+// The statistics of a row: mean, 1 / deviation.
+__device__ __forceinline__ void put_stats(uint64_t stats, uint32_t row, float mean, float rstd) {
+  G<float>(stats)[static_cast<uint64_t>(row) * 2] = mean;
+  G<float>(stats)[static_cast<uint64_t>(row) * 2 + 1] = rstd;
+}
+__device__ __forceinline__ float2 get_stats(uint64_t stats, uint32_t row) {
+  const auto* p = G<const float>(stats) + static_cast<uint64_t>(row) * 2;
+  return make_float2(p[0], p[1]);
+}
+
 struct Forward {
   uint64_t x, residual, weight, bias, y, h, stats;
-  int64_t x_stride, residual_stride;      // in elements
+  uint64_t x_row, residual_row;           // bytes from row to row
   uint32_t rows, cols;
   int32_t weight_dtype;
   float eps;
   DropSpec drop;
 };
 
+constexpr int norm_threads(int lanes) { return lanes > 256 ? lanes : 256; }
+constexpr int norm_back_threads(int lanes) { return lanes > 512 ? lanes : lanes == 256 ? 256 : 512; }
+
+// The row of a workgroup's rows that a lane belongs to: the same in a wave
+// unless several share it, so that addresses of rows stay in scalar registers.
+template <int LANES>
+__device__ __forceinline__ uint32_t row_of_lane() {
+  const uint32_t r = threadIdx.x / LANES;
+  return LANES >= 64 ? __builtin_amdgcn_readfirstlane(r) : r;
+}
+
+// Columns of the group at c that exist: TAIL false where rows are a multiple of eight.
+template <bool TAIL>
+__device__ __forceinline__ int left_of(uint32_t cols, uint32_t c) {
+  return c >= cols ? 0 : TAIL ? static_cast<int>(min(cols - c, 8u)) : 8;
+}
+
 // z of elements c .. c+7 of a row: what the norm is taken of, in fp32.
-template <int D, bool FUSED>
-__device__ __forceinline__ v8f input8(const Forward& a, int64_t row, uint32_t c, uint64_t offset) {
-  typedef typename Of<D>::one one;
-  const int64_t left = static_cast<int64_t>(a.cols) - c;
-  v8f z = load8<D>(a.x + (row * a.x_stride + c) * sizeof(one), left);
+template <int D, bool FUSED, bool TAIL>
+__device__ __forceinline__ v8f input8(const Forward& a, uint32_t row, uint32_t c, int left, uint64_t offset) {
+  constexpr uint32_t size = sizeof(typename Of<D>::one);
+  Raw<D> r = {};
+  if (FUSED && a.residual != 0) r = load_raw<D, TAIL>(a.residual + row * a.residual_row + c * size, left);
+  v8f z = widen<D>(load_raw<D, TAIL>(a.x + row * a.x_row + c * size, left));
   if constexpr (FUSED) {
     if (a.drop.limit != 0) z = drop8(z, static_cast<uint64_t>(row) * a.cols + c, offset, a.drop);
-    if (a.residual != 0) z = z + load8<D>(a.residual + (row * a.residual_stride + c) * sizeof(one), left);
+    if (a.residual != 0) z = z + widen<D>(r);
   }
   return z;
 }
@@ -89,65 +117,56 @@ __device__ __forceinline__ v8f input8(const Forward& a, int64_t row, uint32_t c,
 // y = (z - mean) rstd w + b. The statistics are those of z in fp32 (the mean
 // first, then the squares of what is left: no cancellation); h, z as the
 // backward pass reads it, is rounded to the type of x for its store only.
-template <int D, int LANES, int K, bool FUSED>
-__global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_forward_kernel(Forward a) {
-  typedef typename Of<D>::one one;
-  constexpr int THREADS = LANES > 256 ? LANES : 256, ROWS = THREADS / LANES;
+template <int D, int LANES, int K, bool FUSED, bool TAIL>
+__global__ __launch_bounds__(norm_threads(LANES)) void norm_forward_kernel(Forward a) {
+  constexpr uint32_t size = sizeof(typename Of<D>::one);
+  constexpr uint32_t ROWS = norm_threads(LANES) / LANES;
   __shared__ float lds[2][LANES > 64 ? LANES / 64 * 2 : 1];
   const uint32_t lane = threadIdx.x % LANES;
   const uint64_t offset = FUSED ? offset_of(a.drop) : 0;
   const float inverse = 1.0f / static_cast<float>(a.cols);
   v8f w[K], b[K];
+  int left[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t c = (lane + k * LANES) * 8;
-    const int64_t left = static_cast<int64_t>(a.cols) - c;
-    const uint32_t size = a.weight_dtype == kF32 ? 4 : 2;
+    left[k] = left_of<TAIL>(a.cols, c);
     w[k] = 1.0f;
     b[k] = 0.0f;
-    if (left > 0 && a.weight != 0) w[k] = load8(a.weight_dtype, a.weight + static_cast<uint64_t>(c) * size, left);
-    if (left > 0 && a.bias != 0) b[k] = load8(a.weight_dtype, a.bias + static_cast<uint64_t>(c) * size, left);
+    if (left[k] > 0 && a.weight != 0) w[k] = load8<TAIL>(a.weight_dtype, a.weight, c, left[k]);
+    if (left[k] > 0 && a.bias != 0) b[k] = load8<TAIL>(a.weight_dtype, a.bias, c, left[k]);
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES; row < a.rows;
-       row += static_cast<int64_t>(gridDim.x) * ROWS) {
+  for (uint32_t row = blockIdx.x * ROWS + row_of_lane<LANES>(); row < a.rows; row += gridDim.x * ROWS) {
     v8f z[K];
     float s[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t c = (lane + k * LANES) * 8;
       z[k] = 0.0f;
-      if (c < a.cols) z[k] = input8<D, FUSED>(a, row, c, offset);
+      if (left[k] > 0) z[k] = input8<D, FUSED, TAIL>(a, row, (lane + k * LANES) * 8, left[k], offset);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) s[0] += total(z[k]);
     row_sum<LANES>(s, lds[0]);
     const float mean = s[0] * inverse;
     float q[1] = {0.0f};
+    const uint64_t at = static_cast<uint64_t>(row) * a.cols * size;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t c = (lane + k * LANES) * 8;
-      if (FUSED && a.h != 0 && c < a.cols)
-        store8<D>(a.h + (row * a.cols + c) * sizeof(one), static_cast<int64_t>(a.cols) - c, z[k]);
+      if (left[k] <= 0) continue;
+      if (FUSED && a.h != 0) store8<D, TAIL>(a.h + at + (lane + k * LANES) * 8 * size, left[k], z[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = z[k][j] - mean;
-        q[0] = __builtin_fmaf(c + j < a.cols ? d : 0.0f, d, q[0]);
+        q[0] = __builtin_fmaf(!TAIL || j < left[k] ? d : 0.0f, d, q[0]);
         z[k][j] = d;
       }
     }
     row_sum<LANES>(q, lds[1]);
     const float rstd = 1.0f / __builtin_sqrtf(q[0] * inverse + a.eps);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const uint32_t c = (lane + k * LANES) * 8;
-      if (c < a.cols)
-        store8<D>(a.y + (row * a.cols + c) * sizeof(one), static_cast<int64_t>(a.cols) - c,
-                  fma8(z[k] * rstd, w[k], b[k]));
-    }
-    if (lane == 0) {
-      G<float>(a.stats)[row * 2] = mean;
-      G<float>(a.stats)[row * 2 + 1] = rstd;
-    }
+    for (int k = 0; k < K; ++k)
+      if (left[k] > 0) store8<D, TAIL>(a.y + at + (lane + k * LANES) * 8 * size, left[k], fma8(z[k] * rstd, w[k], b[k]));
+    if (lane == 0) put_stats(a.stats, row, mean, rstd);
   }
 }
 
@@ -155,40 +174,39 @@ constexpr int kLong = 1024;   // threads for a row that no shape holds in regist
 
 template <int D, bool FUSED>
 __global__ __launch_bounds__(kLong) void norm_forward_long_kernel(Forward a) {
-  typedef typename Of<D>::one one;
+  constexpr uint32_t size = sizeof(typename Of<D>::one);
   __shared__ float lds[2][kLong / 64 * 2];
   const uint64_t offset = FUSED ? offset_of(a.drop) : 0;
   const float inverse = 1.0f / static_cast<float>(a.cols);
-  const uint32_t size = a.weight_dtype == kF32 ? 4 : 2;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  auto z8 = [&](uint32_t row, uint32_t c) {
+    return input8<D, FUSED, true>(a, row, c, left_of<true>(a.cols, c), offset);
+  };
+  for (uint32_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     float s[1] = {0.0f}, q[1] = {0.0f};
-    for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) s[0] += total(input8<D, FUSED>(a, row, c, offset));
+    const uint64_t at = static_cast<uint64_t>(row) * a.cols * size;
+    for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) s[0] += total(z8(row, c));
     row_sum<kLong>(s, lds[0]);
     const float mean = s[0] * inverse;
     for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) {
-      const v8f z = input8<D, FUSED>(a, row, c, offset);
-      if (FUSED && a.h != 0)
-        store8<D>(a.h + (row * a.cols + c) * sizeof(one), static_cast<int64_t>(a.cols) - c, z);
+      const v8f z = z8(row, c);
+      const int left = left_of<true>(a.cols, c);
+      if (FUSED && a.h != 0) store8<D>(a.h + at + c * size, left, z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = c + j < a.cols ? z[j] - mean : 0.0f;
+        const float d = j < left ? z[j] - mean : 0.0f;
         q[0] = __builtin_fmaf(d, d, q[0]);
       }
     }
     row_sum<kLong>(q, lds[1]);
     const float rstd = 1.0f / __builtin_sqrtf(q[0] * inverse + a.eps);
     for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) {
-      const int64_t left = static_cast<int64_t>(a.cols) - c;
+      const int left = left_of<true>(a.cols, c);
       v8f w = 1.0f, b = 0.0f;
-      if (a.weight != 0) w = load8(a.weight_dtype, a.weight + static_cast<uint64_t>(c) * size, left);
-      if (a.bias != 0) b = load8(a.weight_dtype, a.bias + static_cast<uint64_t>(c) * size, left);
-      store8<D>(a.y + (row * a.cols + c) * sizeof(one), left,
-                fma8((input8<D, FUSED>(a, row, c, offset) - mean) * rstd, w, b));
+      if (a.weight != 0) w = load8<true>(a.weight_dtype, a.weight, c, left);
+      if (a.bias != 0) b = load8<true>(a.weight_dtype, a.bias, c, left);
+      store8<D>(a.y + at + c * size, left, fma8((z8(row, c) - mean) * rstd, w, b));
     }
-    if (threadIdx.x == 0) {
-      G<float>(a.stats)[row * 2] = mean;
-      G<float>(a.stats)[row * 2 + 1] = rstd;
-    }
+    if (threadIdx.x == 0) put_stats(a.stats, row, mean, rstd);
   }
 }
 
@@ -201,75 +219,98 @@ __global__ __launch_bounds__(kLong) void norm_forward_long_kernel(Forward a) {
 // up: no atomics, so the same bits on every run.
 struct Backward {
   uint64_t dy, h, stats, grad_h, weight, dh, dx;
-  int64_t dy_stride, h_stride, grad_h_stride;   // in elements
+  uint64_t dy_row, h_row, grad_h_row;           // bytes from row to row
   float* partials;                              // [workgroup][dweight, dbias][cols], or NULL
   uint32_t rows, cols;
   int32_t weight_dtype;
   DropSpec drop;
 };
 
-template <int D>
-__device__ __forceinline__ void store_grads(const Backward& a, int64_t row, uint32_t c, int64_t left, v8f d,
+template <int D, bool TAIL>
+__device__ __forceinline__ void store_grads(const Backward& a, uint32_t row, uint32_t c, int left, v8f d,
                                             uint64_t offset) {
-  typedef typename Of<D>::one one;
-  if (a.grad_h != 0) d = d + load8<D>(a.grad_h + (row * a.grad_h_stride + c) * sizeof(one), left);
-  const uint64_t at = (row * a.cols + c) * sizeof(one);
-  store8<D>(a.dh + at, left, d);
-  if (a.drop.limit != 0) store8<D>(a.dx + at, left, drop8(d, static_cast<uint64_t>(row) * a.cols + c, offset, a.drop));
+  constexpr uint32_t size = sizeof(typename Of<D>::one);
+  const uint64_t at = static_cast<uint64_t>(row) * a.cols * size;
+  if (a.grad_h != 0) d = d + widen<D>(load_raw<D, TAIL>(a.grad_h + row * a.grad_h_row + c * size, left));
+  store8<D, TAIL>(a.dh + at + c * size, left, d);
+  if (a.drop.limit != 0) {
+    d = drop8(d, static_cast<uint64_t>(row) * a.cols + c, offset, a.drop);
+    store8<D, TAIL>(a.dx + at + c * size, left, d);
+  }
 }
 
-template <int D, int LANES, int K>
-__global__ __launch_bounds__(LANES == 1024 ? 1024 : LANES == 256 ? 256 : 512) void norm_backward_kernel(Backward a) {
-  typedef typename Of<D>::one one;
-  constexpr int THREADS = LANES == 1024 ? 1024 : LANES == 256 ? 256 : 512, ROWS = THREADS / LANES;
+// The next row is loaded while this one is worked on (8192 x 8192 in fp32: 195 us,
+// 199 without), except by 1024 lanes, whose 128 registers do not hold it, nor the
+// weights.
+template <int D, int LANES, int K, bool TAIL>
+__global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel(Backward a) {
+  constexpr uint32_t size = sizeof(typename Of<D>::one);
+  constexpr uint32_t THREADS = norm_back_threads(LANES), ROWS = THREADS / LANES;
+  constexpr bool AHEAD = LANES < 1024;
   __shared__ float lds[2][LANES > 64 ? LANES / 64 * 2 : 1];
-  const uint32_t lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
+  const uint32_t lane = threadIdx.x % LANES, mine = row_of_lane<LANES>(), step = gridDim.x * ROWS;
   const uint64_t offset = offset_of(a.drop);
   const float inverse = 1.0f / static_cast<float>(a.cols);
-  const uint32_t size = a.weight_dtype == kF32 ? 4 : 2;
   v8f w[K], dw[K], db[K];
+  int left[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t c = (lane + k * LANES) * 8;
+    left[k] = left_of<TAIL>(a.cols, c);
     w[k] = 1.0f;
     dw[k] = db[k] = 0.0f;
-    if (c < a.cols && a.weight != 0)
-      w[k] = load8(a.weight_dtype, a.weight + static_cast<uint64_t>(c) * size, static_cast<int64_t>(a.cols) - c);
+    if (AHEAD && left[k] > 0 && a.weight != 0) w[k] = load8<TAIL>(a.weight_dtype, a.weight, c, left[k]);
   }
-  int turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + mine; row < a.rows;
-       row += static_cast<int64_t>(gridDim.x) * ROWS, turn ^= 1) {
-    const float mean = G<const float>(a.stats)[row * 2], rstd = G<const float>(a.stats)[row * 2 + 1];
-    v8f g[K], n[K];
-    float s[2] = {0.0f, 0.0f};
+  auto weigh = [&](int k, v8f x) __attribute__((always_inline)) {
+    if constexpr (AHEAD) return x * w[k];
+    if (left[k] <= 0 || a.weight == 0) return x;
+    return x * load8<TAIL>(a.weight_dtype, a.weight, (lane + k * LANES) * 8, left[k]);
+  };
+  Raw<D> dy_next[K], h_next[K];
+  float2 stats_next = {};
+  auto fetch = [&](uint32_t r) __attribute__((always_inline)) {
+    stats_next = get_stats(a.stats, r);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const uint32_t c = (lane + k * LANES) * 8;
-      const int64_t left = static_cast<int64_t>(a.cols) - c;
-      g[k] = n[k] = 0.0f;
-      if (left > 0) {
-        g[k] = load8<D>(a.dy + (row * a.dy_stride + c) * sizeof(one), left);
-        n[k] = load8<D>(a.h + (row * a.h_stride + c) * sizeof(one), left);
-      }
+      dy_next[k] = h_next[k] = Raw<D>{};
+      if (left[k] <= 0) continue;
+      dy_next[k] = load_raw<D, TAIL>(a.dy + r * a.dy_row + c * size, left[k]);
+      h_next[k] = load_raw<D, TAIL>(a.h + r * a.h_row + c * size, left[k]);
     }
+  };
+  uint32_t row = blockIdx.x * ROWS + mine;
+  if (row < a.rows) fetch(row);
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    const float mean = stats_next.x, rstd = stats_next.y;
+    Raw<D> dy[K], h[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      n[k] = (n[k] - mean) * rstd;
-      dw[k] = fma8(g[k], n[k], dw[k]);
-      db[k] = db[k] + g[k];
-      g[k] = g[k] * w[k];
-      s[0] += total(g[k]);
-      s[1] += total(g[k] * n[k]);
+      dy[k] = dy_next[k];
+      h[k] = h_next[k];
+    }
+    if (AHEAD && row + step < a.rows) fetch(row + step);
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (!AHEAD) __builtin_amdgcn_sched_barrier(0);
+      const v8f n = (widen<D>(h[k]) - mean) * rstd, d = widen<D>(dy[k]), g = weigh(k, d);
+      dw[k] = fma8(d, n, dw[k]);
+      db[k] = db[k] + d;
+      s[0] += total(g);
+      s[1] += total(g * n);
     }
     row_sum<LANES>(s, lds[turn]);
     s[0] *= inverse;
     s[1] *= inverse;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t c = (lane + k * LANES) * 8;
-      const int64_t left = static_cast<int64_t>(a.cols) - c;
-      if (left > 0) store_grads<D>(a, row, c, left, (fma8(n[k], v8f(-s[1]), g[k]) - s[0]) * rstd, offset);
+      if (!AHEAD) __builtin_amdgcn_sched_barrier(0);
+      const v8f n = (widen<D>(h[k]) - mean) * rstd, g = weigh(k, widen<D>(dy[k]));
+      if (left[k] > 0)
+        store_grads<D, TAIL>(a, row, (lane + k * LANES) * 8, left[k], (fma8(n, v8f(-s[1]), g) - s[0]) * rstd, offset);
     }
+    if (!AHEAD && row + step < a.rows) fetch(row + step);
   }
   if (a.partials == nullptr) return;
   float* to = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
@@ -308,26 +349,25 @@ __global__ __launch_bounds__(LANES == 1024 ? 1024 : LANES == 256 ? 256 : 512) vo
 
 template <int D>
 __global__ __launch_bounds__(kLong) void norm_backward_long_kernel(Backward a) {
-  typedef typename Of<D>::one one;
+  constexpr uint32_t size = sizeof(typename Of<D>::one);
   __shared__ float lds[2][kLong / 64 * 2];
   const uint64_t offset = offset_of(a.drop);
   const float inverse = 1.0f / static_cast<float>(a.cols);
-  const uint32_t size = a.weight_dtype == kF32 ? 4 : 2;
   float* to = a.partials == nullptr ? nullptr : a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
   bool first = true;
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false, turn ^= 1) {
-    const float mean = G<const float>(a.stats)[row * 2], rstd = G<const float>(a.stats)[row * 2 + 1];
+  for (uint32_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false, turn ^= 1) {
+    const float2 stats = get_stats(a.stats, row);
     float s[2] = {0.0f, 0.0f};
     for (int pass = 0; pass < 2; ++pass) {
       for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) {
-        const int64_t left = static_cast<int64_t>(a.cols) - c;
-        const v8f dy = load8<D>(a.dy + (row * a.dy_stride + c) * sizeof(one), left);
-        const v8f n = (load8<D>(a.h + (row * a.h_stride + c) * sizeof(one), left) - mean) * rstd;
+        const int left = left_of<true>(a.cols, c);
+        const v8f dy = load8<D>(a.dy + row * a.dy_row + c * size, left);
+        const v8f n = (load8<D>(a.h + row * a.h_row + c * size, left) - stats.x) * stats.y;
         v8f g = dy;
-        if (a.weight != 0) g = g * load8(a.weight_dtype, a.weight + static_cast<uint64_t>(c) * size, left);
+        if (a.weight != 0) g = g * load8<true>(a.weight_dtype, a.weight, c, left);
         if (pass == 1) {
-          store_grads<D>(a, row, c, left, (fma8(n, v8f(-s[1]), g) - s[0]) * rstd, offset);
+          store_grads<D, true>(a, row, c, left, (fma8(n, v8f(-s[1]), g) - s[0]) * stats.y, offset);
           continue;
         }
         s[0] += total(g);
@@ -438,40 +478,51 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(Drop a) {
 
 uint64_t addr(const void* p) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p)); }
 
+uint64_t bytes(int64_t stride, int32_t dtype) { return static_cast<uint64_t>(stride * dtype_size(dtype)); }
+
 unsigned grid_of(int64_t want, int64_t most) {
   return static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most);
 }
 
+// f(lanes, groups) with the row's shape as constants; false if there is none.
+template <typename F>
+bool by_shape(int64_t cols, F f) {
+  const NormShape s = norm_shape(cols);
+  auto is = [&](auto lanes, auto groups) {
+    if (s.lanes != lanes.value || s.groups != groups.value) return false;
+    f(lanes, groups);
+    return true;
+  };
+  constexpr std::integral_constant<int, 1> one;
+  constexpr std::integral_constant<int, 2> two;
+  return is(std::integral_constant<int, 16>(), one) || is(std::integral_constant<int, 64>(), one) ||
+         is(std::integral_constant<int, 64>(), two) || is(std::integral_constant<int, 256>(), one) ||
+         is(std::integral_constant<int, 256>(), two) || is(std::integral_constant<int, 512>(), two) ||
+         is(std::integral_constant<int, 1024>(), two);
+}
+
 template <int D, bool FUSED>
 void launch_forward(const Forward& a, hipStream_t s) {
-  const NormShape shape = norm_shape(a.cols);
   auto go = [&](auto kernel, int threads, int rows) {
     hipLaunchKernelGGL(kernel, dim3(grid_of((int64_t(a.rows) + rows - 1) / rows, 2048)), dim3(threads), 0, s, a);
   };
-  if (shape.lanes == 16) go(norm_forward_kernel<D, 16, 1, FUSED>, 256, 16);
-  else if (shape.lanes == 64 && shape.groups == 1) go(norm_forward_kernel<D, 64, 1, FUSED>, 256, 4);
-  else if (shape.lanes == 64) go(norm_forward_kernel<D, 64, 2, FUSED>, 256, 4);
-  else if (shape.lanes == 256 && shape.groups == 1) go(norm_forward_kernel<D, 256, 1, FUSED>, 256, 1);
-  else if (shape.lanes == 256) go(norm_forward_kernel<D, 256, 2, FUSED>, 256, 1);
-  else if (shape.lanes == 1024 && shape.groups == 1) go(norm_forward_kernel<D, 1024, 1, FUSED>, 1024, 1);
-  else if (shape.lanes == 1024) go(norm_forward_kernel<D, 1024, 2, FUSED>, 1024, 1);
-  else go(norm_forward_long_kernel<D, FUSED>, kLong, 1);
+  const bool short_row = by_shape(a.cols, [&](auto lanes, auto groups) {
+    constexpr int L = decltype(lanes)::value, K = decltype(groups)::value, T = norm_threads(L);
+    if (a.cols % 8 != 0) go(norm_forward_kernel<D, L, K, FUSED, true>, T, T / L);
+    else go(norm_forward_kernel<D, L, K, FUSED, false>, T, T / L);
+  });
+  if (!short_row) go(norm_forward_long_kernel<D, FUSED>, kLong, 1);
 }
 
 template <int D>
 void launch_backward(const Backward& a, unsigned blocks, hipStream_t s) {
-  const NormShape shape = norm_shape(a.cols);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(norm_backward_threads(shape)), 0, s, a);
-  };
-  if (shape.lanes == 16) go(norm_backward_kernel<D, 16, 1>);
-  else if (shape.lanes == 64 && shape.groups == 1) go(norm_backward_kernel<D, 64, 1>);
-  else if (shape.lanes == 64) go(norm_backward_kernel<D, 64, 2>);
-  else if (shape.lanes == 256 && shape.groups == 1) go(norm_backward_kernel<D, 256, 1>);
-  else if (shape.lanes == 256) go(norm_backward_kernel<D, 256, 2>);
-  else if (shape.lanes == 1024 && shape.groups == 1) go(norm_backward_kernel<D, 1024, 1>);
-  else if (shape.lanes == 1024) go(norm_backward_kernel<D, 1024, 2>);
-  else go(norm_backward_long_kernel<D>);
+  auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(threads), 0, s, a); };
+  const bool short_row = by_shape(a.cols, [&](auto lanes, auto groups) {
+    constexpr int L = decltype(lanes)::value, K = decltype(groups)::value, T = norm_back_threads(L);
+    if (a.cols % 8 != 0) go(norm_backward_kernel<D, L, K, true>, T);
+    else go(norm_backward_kernel<D, L, K, false>, T);
+  });
+  if (!short_row) go(norm_backward_long_kernel<D>, kLong);
 }
 
 template <typename F>
@@ -486,7 +537,7 @@ class HipLayersDevice final : public LayersDevice {
   int norm_forward(const NormForwardArgs& a, std::string* err) override {
     if (a.rows == 0) return kOk;
     const Forward f = {addr(a.x.data), addr(a.residual.data), addr(a.weight), addr(a.bias), addr(a.y), addr(a.h),
-                       addr(a.stats), a.x.stride, a.residual.stride, static_cast<uint32_t>(a.rows),
+                       addr(a.stats), bytes(a.x.stride, a.dtype), bytes(a.residual.stride, a.dtype), static_cast<uint32_t>(a.rows),
                        static_cast<uint32_t>(a.cols), a.weight_dtype, static_cast<float>(a.eps), a.drop};
     hipStream_t s = static_cast<hipStream_t>(a.stream);
     by_type(a.dtype, [&](auto d) {
@@ -503,7 +554,8 @@ class HipLayersDevice final : public LayersDevice {
     const int32_t blocks = norm_backward_blocks(a.rows, a.cols);
     if (a.rows > 0) {
       const Backward b = {addr(a.dy.data), addr(a.h.data), addr(a.stats), addr(a.grad_h.data), addr(a.weight),
-                          addr(a.dh), addr(a.dx), a.dy.stride, a.h.stride, a.grad_h.stride,
+                          addr(a.dh), addr(a.dx), bytes(a.dy.stride, a.dtype), bytes(a.h.stride, a.dtype),
+                          bytes(a.grad_h.stride, a.dtype),
                           weights ? static_cast<float*>(a.workspace) : nullptr, static_cast<uint32_t>(a.rows),
                           static_cast<uint32_t>(a.cols), a.weight_dtype, a.drop};
       by_type(a.dtype, [&](auto d) { launch_backward<decltype(d)::value>(b, static_cast<unsigned>(blocks), s); });

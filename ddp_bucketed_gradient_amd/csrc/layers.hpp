@@ -109,18 +109,19 @@ NormShape norm_shape(int64_t cols);
 // weights' gradients: a function of the sizes only, so that the order of the
 // sums does not depend on the device.
 int32_t norm_backward_blocks(int64_t rows, int64_t cols);
-int norm_backward_threads(NormShape s);
 
 // How the embedding's gradient is cut.
 constexpr int kSortThreads = 1024;
 constexpr int kSortKeys = 4;                                  // keys of a thread
 constexpr int64_t kSortTile = kSortThreads * kSortKeys;       // keys of a workgroup
+constexpr int64_t kRangeKeys = 16384;                         // most tokens of a sort in one launch
+constexpr int kRanges = 32;                                   // workgroups of it
 constexpr int kMaxDigit = 10;                                 // bits that one pass sorts by
 constexpr int64_t kScanTiles = 64;                            // more tiles than this are scanned by a kernel of their own
 
 struct LookupPlan {
   int passes, digit;        // passes of the sort, bits of each
-  int64_t tiles;            // workgroups of the sort
+  int64_t tiles;            // workgroups of the sort; 0: one launch by ranges of tokens
   int64_t unit, units;      // sorted places of a unit of the sum, units
   // byte offsets into the workspace
   int64_t keys[2], order[2], hist, totals, joins, list, partials, bytes;

@@ -150,8 +150,10 @@ def test_workspaces_stay_in_bounds(lib):
         assert 2 * cols * 4 <= b <= 1 << 28 and b % 256 == 0
     for n, vocab, cols in [(0, 0, 1), (1, 1, 1), (16384, 30522, 1024), (1 << 30, (1 << 31) - 2, 1), (1 << 16, 5, 1 << 24)]:
         b = lib.embedding_backward_workspace_bytes(n, vocab, cols)
-        # keys and order twice; histograms of at most 1024 counters for 4096 keys; partial sums of at most 4096 units
-        assert 16 * n <= b <= 16 * n + (n // 4096 + 1) * 4096 + 8192 * 4 * cols + 32768 and b % 256 == 0
+        # keys and order twice; histograms of at most 1024 counters for 4096 keys; two partial sums for each unit of
+        # 8 or more places, of which there are at most 65536
+        units = min(n // 8 + 1, 65536)
+        assert 16 * n <= b <= 16 * n + (n // 4096 + 1) * 4096 + units * (8 * cols + 4) + 32768 and b % 256 == 0
 
 
 def test_null_results(lib):

@@ -16,49 +16,50 @@ __device__ __forceinline__ uint32_t token_at(uint64_t tokens, int32_t bytes, int
 }
 
 // ---------------------------------------------------------------------------
-// y_i = scale table[t_i] + residual_i, in fp32, rounded once. The groups of
-// eight elements of all rows are counted through; a workgroup takes kTile of
-// them at a time.
+// y_i = scale table[t_i] + residual_i, in fp32, rounded once.
 struct Lookup {
   uint64_t tokens, table, residual, y;
-  int64_t groups, residual_stride;
-  uint32_t row_groups, cols, vocab;
+  uint64_t residual_row;        // bytes from row to row
+  uint32_t n, cols, vocab, slice;
   int32_t token_bytes;
   float scale;
 };
-constexpr int kThreads = 256, kUnroll = 2, kTile = kThreads * kUnroll;
 
-template <int TD, int D>
-__global__ __launch_bounds__(kThreads) void lookup_kernel(Lookup a) {
-  typedef typename Of<D>::one one;
-  typedef typename Of<TD>::one table_one;
-  for (int64_t tile = static_cast<int64_t>(blockIdx.x) * kTile; tile < a.groups;
-       tile += static_cast<int64_t>(gridDim.x) * kTile) {
-    const int64_t row0 = tile / a.row_groups;
-    const uint32_t rest = static_cast<uint32_t>(tile - row0 * a.row_groups);
-    uint32_t c[kUnroll], t[kUnroll];
-    int64_t row[kUnroll];
-    v8f x[kUnroll], r[kUnroll];
+// A wave takes kRows rows of one slice, 64 groups of eight columns or less, so
+// that tokens and row addresses are uniform. Rows of 16 groups and less share a
+// wave: PACK of them, side by side.
+constexpr int kRows = 4;
+template <int TD, int D, int PACK, bool TAIL>
+__global__ __launch_bounds__(256) void lookup_kernel(Lookup a) {
+  constexpr uint32_t size = sizeof(typename Of<D>::one), table_size = sizeof(typename Of<TD>::one);
+  constexpr uint32_t LANES = 64 / PACK;
+  const uint32_t lane = threadIdx.x % LANES;
+  const uint32_t c = (blockIdx.y * a.slice + lane) * 8;
+  const int left = lane >= a.slice || c >= a.cols ? 0 : TAIL ? static_cast<int>(min(a.cols - c, 8u)) : 8;
+  if (left <= 0) return;
+  const uint32_t part = PACK > 1 ? threadIdx.x / LANES : __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
+  for (uint32_t first = (blockIdx.x * (256 / LANES) + part) * kRows; first < a.n; first += gridDim.x * (256 / LANES) * kRows) {
+    uint32_t t[kRows];
+    Raw<TD> x[kRows];
+    Raw<D> r[kRows];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t i = u * kThreads + threadIdx.x, q = (rest + i) / a.row_groups;
-      row[u] = row0 + q;
-      c[u] = (rest + i - q * a.row_groups) * 8;
-      t[u] = a.vocab;
-      x[u] = r[u] = 0.0f;
-      if (tile + i < a.groups) {
-        t[u] = token_at(a.tokens, a.token_bytes, row[u], a.vocab);
-        if (a.residual != 0) r[u] = load8<D>(a.residual + (row[u] * a.residual_stride + c[u]) * sizeof(one), static_cast<int64_t>(a.cols) - c[u]);
-      }
+    for (int k = 0; k < kRows; ++k)
+      t[k] = first + k < a.n ? token_at(a.tokens, a.token_bytes, first + k, a.vocab) : a.vocab;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      x[k] = Raw<TD>{};
+      r[k] = Raw<D>{};
+      if (t[k] < a.vocab) x[k] = load_raw<TD, TAIL>(a.table + static_cast<uint64_t>(t[k]) * a.cols * table_size + c * table_size, left);
+      if (a.residual != 0 && first + k < a.n) r[k] = load_raw<D, TAIL>(a.residual + (first + k) * a.residual_row + c * size, left);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (t[u] < a.vocab)
-        x[u] = load8<TD>(a.table + (static_cast<uint64_t>(t[u]) * a.cols + c[u]) * sizeof(table_one), static_cast<int64_t>(a.cols) - c[u]) * a.scale;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (tile + u * kThreads + threadIdx.x < a.groups)
-        store8<D>(a.y + (static_cast<uint64_t>(row[u]) * a.cols + c[u]) * sizeof(one), static_cast<int64_t>(a.cols) - c[u], x[u] + r[u]);
+    for (int k = 0; k < kRows; ++k) {
+      if (first + k >= a.n) break;
+      v8f y = 0.0f;
+      if (t[k] < a.vocab) y = widen<TD>(x[k]) * a.scale;
+      if (a.residual != 0) y = y + widen<D>(r[k]);
+      store8<D, TAIL>(a.y + static_cast<uint64_t>(first + k) * a.cols * size + c * size, left, y);
+    }
   }
 }
 
@@ -204,111 +205,20 @@ __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* waves) {
 
 // All of the sort in one launch, for up to kRangeKeys tokens. Workgroup g of
 // kRanges takes the tokens t with t % kRanges = g (so that neighbouring common
-// ones do not meet in one), finds them among all, and sorts them by t / kRanges
-// in LDS, six bits a pass, one counter of a wave's digits to a thread. What it
-// counts of the ranges before its own is where its places begin. The order is
-// one of groups: t % kRanges, then t.
-constexpr int kRangeBits = 6;
+// ones do not meet in one), finds their places among all, and sorts those by t /
+// kRanges in LDS, six bits a pass, one counter of a wave's digits to a thread.
+// What it counts of the ranges before its own is where its places begin. The
+// order is one of groups: t % kRanges, then t. The loops are not unrolled: few
+// keys pass through them, and 24 KB of unrolled code took longer to fetch than
+// they to run.
+constexpr int kRangeBits = 6, kDigits = 1 << kRangeBits;
 struct RangeLds {
-  uint32_t keys[kRangeKeys];
-  uint16_t places[kRangeKeys];
-  uint16_t count[kWaves << kRangeBits];     // [digit][wave]
+  uint32_t token[kRangeKeys];
+  uint16_t place[2][kRangeKeys];
+  uint32_t count[kDigits * kWaves];         // [digit][wave]
   uint32_t waves[kWaves];
   uint2 here[kWaves];                       // of each wave: tokens of the range, and of those before it
 };
-
-// Collects a range's tokens, in their order, E of all tokens to a lane; returns
-// where the range's places begin and how many there are.
-template <int E>
-__device__ __forceinline__ uint2 collect(const Sort& a, RangeLds& s) {
-  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, range = blockIdx.x;
-  const uint32_t n = static_cast<uint32_t>(a.n), each = (n + kSortThreads - 1) / kSortThreads;
-  const uint32_t at = wave * 64 * each + lane;     // a wave's share is consecutive: 64 * each
-  uint32_t key[E], total = 0, below = 0;
-  auto read = [&](auto token) __attribute__((always_inline)) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      key[e] = a.vocab;
-      if (e < static_cast<int>(each) && at + e * 64 < n) {
-        const auto t = G<const decltype(token)>(a.tokens)[at + e * 64];
-        key[e] = t < a.vocab ? static_cast<uint32_t>(t) : a.vocab;
-      }
-    }
-  };
-  if (a.token_bytes == 4) read(uint32_t());
-  else read(uint64_t());
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    total += __popcll(__ballot(key[e] < a.vocab && key[e] % kRanges == range));
-    below += __popcll(__ballot(key[e] < a.vocab && key[e] % kRanges < range));
-  }
-  if (lane == 0) s.here[wave] = make_uint2(total, below);
-  __syncthreads();
-  uint32_t to = 0, m = 0, first = 0;
-#pragma unroll
-  for (uint32_t w = 0; w < static_cast<uint32_t>(kWaves); ++w) {
-    if (w < wave) to += s.here[w].x;
-    m += s.here[w].x;
-    first += s.here[w].y;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const bool in = key[e] < a.vocab && key[e] % kRanges == range;
-    const uint64_t all = __ballot(in);
-    if (in) {
-      const uint32_t i = to + __popcll(all & ((uint64_t(1) << lane) - 1));
-      s.keys[i] = key[e] / kRanges;
-      s.places[i] = static_cast<uint16_t>(at + e * 64);
-    }
-    to += __popcll(all);
-  }
-  return make_uint2(first, m);
-}
-
-// One pass over the m keys of a range, M of them to a lane.
-template <int M>
-__device__ __forceinline__ void sort_range(const Sort& a, RangeLds& s, uint32_t first, uint32_t m, int shift, bool final) {
-  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, mine = (m + kSortThreads - 1) / kSortThreads;
-  const uint32_t at = wave * 64 * mine + lane;
-  uint32_t key[M], place[M], rank[M];
-  s.count[threadIdx.x] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < M; ++e) {
-    const bool there = e < static_cast<int>(mine) && at + e * 64 < m;
-    key[e] = place[e] = rank[e] = 0;
-    if (there) {
-      key[e] = s.keys[at + e * 64];
-      place[e] = s.places[at + e * 64];
-    }
-    const uint32_t d = key[e] >> shift & ((1u << kRangeBits) - 1);
-    const uint64_t same = equal_digits<kRangeBits>(d, there), lower = same & ((uint64_t(1) << lane) - 1);
-    if (there) {
-      const uint32_t before = s.count[d * kWaves + wave];
-      rank[e] = before + __popcll(lower);
-      wave_fence();
-      if (lower == 0) s.count[d * kWaves + wave] = static_cast<uint16_t>(before + __popcll(same));
-    }
-    wave_fence();
-  }
-  __syncthreads();
-  const uint32_t before = scan(s.count[threadIdx.x], s.waves);
-  s.count[threadIdx.x] = static_cast<uint16_t>(before);
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < M; ++e) {
-    if (e >= static_cast<int>(mine) || at + e * 64 >= m) continue;
-    const uint32_t to = s.count[(key[e] >> shift & ((1u << kRangeBits) - 1)) * kWaves + wave] + rank[e];
-    if (final) {
-      a.keys[first + to] = key[e] * kRanges + blockIdx.x;
-      a.order[first + to] = place[e];
-    } else {
-      s.keys[to] = key[e];
-      s.places[to] = static_cast<uint16_t>(place[e]);
-    }
-  }
-  __syncthreads();
-}
 
 __global__ __launch_bounds__(kSortThreads) void sort_ranges_kernel(Sort a) {
   extern __shared__ char raw_lds[];
@@ -317,17 +227,69 @@ __global__ __launch_bounds__(kSortThreads) void sort_ranges_kernel(Sort a) {
     return;
   }
   RangeLds& s = *reinterpret_cast<RangeLds*>(raw_lds);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.joins = 0;
-  const uint2 got = a.n <= 4 * kSortThreads ? collect<4>(a, s) : collect<kRangeKeys / kSortThreads>(a, s);
-  const uint32_t first = got.x, m = got.y;
-  // behind the last range: the tokens outside of the table
-  if (blockIdx.x == kRanges - 1)
-    for (uint32_t i = first + m + threadIdx.x; i < a.n; i += kSortThreads) a.keys[i] = a.vocab;
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, range = blockIdx.x, n = static_cast<uint32_t>(a.n);
+  const uint64_t under = (uint64_t(1) << lane) - 1;
+  if (range == 0 && threadIdx.x == 0) *a.joins = 0;
+  // a wave's share of the tokens is consecutive
+  const uint32_t each = (n + kSortThreads - 1) / kSortThreads * 64, from = wave * each, to = min(from + each, n);
+#pragma unroll 4
+  for (uint32_t i = from + lane; i < to; i += 64) s.token[i] = token_at(a.tokens, a.token_bytes, i, a.vocab);
+  uint32_t mine = 0, below = 0;
+  for (uint32_t i = from; i < to; i += 64) {
+    const uint32_t t = i + lane < to ? s.token[i + lane] : a.vocab;
+    mine += __popcll(__ballot(t < a.vocab && t % kRanges == range));
+    below += __popcll(__ballot(t < a.vocab && t % kRanges < range));
+  }
+  if (lane == 0) s.here[wave] = make_uint2(mine, below);
   __syncthreads();
+  uint32_t at = 0, m = 0, first = 0;               // first: where the range's places begin; m: how many
+  for (uint32_t w = 0; w < static_cast<uint32_t>(kWaves); ++w) {
+    const uint2 h = s.here[w];
+    at += w < wave ? h.x : 0;
+    m += h.x;
+    first += h.y;
+  }
+  for (uint32_t i = from; i < to; i += 64) {
+    const uint32_t t = i + lane < to ? s.token[i + lane] : a.vocab;
+    const uint64_t in = __ballot(t < a.vocab && t % kRanges == range);
+    if (in >> lane & 1) s.place[0][at + __popcll(in & under)] = static_cast<uint16_t>(i + lane);
+    at += __popcll(in);
+  }
+  // behind the last range: the tokens outside of the table
+  if (range == kRanges - 1)
+    for (uint32_t i = first + m + threadIdx.x; i < n; i += kSortThreads) a.keys[i] = a.vocab;
+
+  const uint32_t share = (m + kSortThreads - 1) / kSortThreads * 64, begin = min(wave * share, m), end = min(begin + share, m);
   for (int pass = 0; pass < a.passes; ++pass) {
-    // few keys, but where one token holds most places: the code of sixteen is long
-    if (m <= kSortThreads) sort_range<1>(a, s, first, m, pass * kRangeBits, pass == a.passes - 1);
-    else sort_range<kRangeKeys / kSortThreads>(a, s, first, m, pass * kRangeBits, pass == a.passes - 1);
+    const int shift = pass * kRangeBits;
+    const uint16_t* in = s.place[pass & 1];
+    uint16_t* out = s.place[~pass & 1];
+    s.count[threadIdx.x] = 0;
+    __syncthreads();
+    for (uint32_t i = begin + lane; i < end; i += 64)
+      atomicAdd(&s.count[(s.token[in[i]] / kRanges >> shift) % kDigits * kWaves + wave], 1u);
+    __syncthreads();
+    const uint32_t before = scan(s.count[threadIdx.x], s.waves);
+    s.count[threadIdx.x] = before;
+    __syncthreads();
+    for (uint32_t i = begin; i < end; i += 64) {   // stable: 64 at a time, each behind the equal ones below it
+      const bool there = i + lane < end;
+      const uint32_t place = there ? in[i + lane] : 0, token = s.token[place];
+      const uint32_t d = (token / kRanges >> shift) % kDigits;
+      const uint64_t same = equal_digits<kRangeBits>(d, there), lower = same & under;
+      const uint32_t base = s.count[d * kWaves + wave], to_place = base + __popcll(lower);
+      wave_fence();
+      if (there && lower == 0) s.count[d * kWaves + wave] = base + __popcll(same);
+      wave_fence();
+      if (!there) continue;
+      if (pass < a.passes - 1) {
+        out[to_place] = static_cast<uint16_t>(place);
+      } else {
+        a.keys[first + to_place] = token;
+        a.order[first + to_place] = place;
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -393,7 +355,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(Sort a) {
       all = a.totals[threadIdx.x];
       before = a.hist[static_cast<int64_t>(blockIdx.x) * bins + threadIdx.x];
     } else {
-#pragma unroll 8
+#pragma unroll 16
       for (uint32_t t = 0; t < a.tiles; ++t) {
         const uint32_t x = a.hist[static_cast<int64_t>(t) * bins + threadIdx.x];
         all += x;
@@ -432,8 +394,10 @@ struct Sum {
   uint64_t dy_row, table_row;   // bytes from row to row
   uint32_t n, unit, units;      // at most 2^30 places
   uint32_t cols, vocab;
+  uint32_t slice;               // groups of eight columns that a wave takes: equal shares, at most 64
   float* partials;              // [unit][run from the left, run to the right][cols]
-  uint32_t *joins, *list;
+  uint32_t* joins;
+  uint2* list;                  // of the long runs: the unit where it begins, its token
   float scale;
 };
 
@@ -457,15 +421,26 @@ template <int D, int GD, bool ADD, bool TAIL>
 __global__ __launch_bounds__(256) void sum_kernel(Sum a) {
   typedef typename Of<D>::one one;
   typedef typename Of<GD>::one grad_one;
-  constexpr int kAhead = ADD ? 4 : 8;
+  constexpr int kAhead = 8;
   const uint32_t u = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (u >= a.units) return;
-  const uint32_t lane = threadIdx.x & 63, c = blockIdx.y * 512 + lane * 8;
-  const int left = c >= a.cols ? 0 : TAIL ? static_cast<int>(min(a.cols - c, 8u)) : 8;
+  const uint32_t lane = threadIdx.x & 63, c = (blockIdx.y * a.slice + lane) * 8;
+  const int left = c >= a.cols || lane >= a.slice ? 0 : TAIL ? static_cast<int>(min(a.cols - c, 8u)) : 8;
   const uint32_t s = u * a.unit, e = min(s + a.unit, a.n), e2 = min(e + a.unit, a.n);
   const uint32_t first = key_at(a, s), last = key_at(a, e - 1);
   const uint32_t before = key_at(a, s > 0 ? s - 1 : 0), unit_before = key_at(a, s > 0 ? s - a.unit : 0);
   const uint32_t behind = key_at(a, e < a.n ? e : e - 1), unit_behind = key_at(a, e2 - 1);
+  uint32_t key, next, place;       // of a lane's place among 64
+  auto window = [&](uint32_t i) {
+    key = next = a.vocab;
+    place = 0;
+    if (i < e2) {
+      key = *G<const uint32_t>(a.keys + static_cast<uint64_t>(i * 4));
+      place = *G<const uint32_t>(a.order + static_cast<uint64_t>(i * 4));
+      if (i + 1 < a.n) next = *G<const uint32_t>(a.keys + static_cast<uint64_t>(i * 4 + 4));
+    }
+  };
+  window(s + lane);
   if (first >= a.vocab) return;
   // the run that comes in from the left: another unit's, unless it covers a whole unit
   const bool from_left = s > 0 && before == first;
@@ -480,13 +455,8 @@ __global__ __launch_bounds__(256) void sum_kernel(Sum a) {
   bool open_left = from_left && mine, pending = false;   // the run in x began in another unit; it has not ended
   for (uint32_t p = s; p < stop; p += 64) {
     const uint32_t i = p + lane;
-    uint32_t key = a.vocab, next = a.vocab, place = 0;
-    if (i < stop) {
-      key = *G<const uint32_t>(a.keys + static_cast<uint64_t>(i * 4));
-      place = *G<const uint32_t>(a.order + static_cast<uint64_t>(i * 4));
-      if (i + 1 < a.n) next = *G<const uint32_t>(a.keys + static_cast<uint64_t>(i * 4 + 4));
-    }
-    const bool ours = key < a.vocab && (mine || key != first) && (i < e || key == last);
+    if (p > s) window(i);
+    const bool ours = i < stop && key < a.vocab && (mine || key != first) && (i < e || key == last);
     const uint64_t todo = __ballot(ours), ends = __ballot(ours && key != next);
     if (todo == 0) continue;
     const int from = __builtin_ctzll(todo), to = 64 - __builtin_clzll(todo);    // they are consecutive
@@ -525,7 +495,7 @@ __global__ __launch_bounds__(256) void sum_kernel(Sum a) {
   }
   if (!pending) return;
   if (left > 0) store8<kF32, TAIL>(partial + (open_left ? 0 : static_cast<uint64_t>(a.cols) * 4), left, x);
-  if (!open_left && c == 0) a.list[atomicAdd(a.joins, 1u)] = u;
+  if (!open_left && c == 0) a.list[atomicAdd(a.joins, 1u)] = make_uint2(u, last);
 }
 
 // The runs that cover whole units: 16 columns to a wave, four to a lane, and 16
@@ -538,9 +508,10 @@ __global__ __launch_bounds__(256) void join_kernel(Sum a) {
   const uint32_t lane = threadIdx.x % kJoinLanes, line = (threadIdx.x & 63) / kJoinLanes, joins = *a.joins;
   const uint32_t c = (blockIdx.y * 4 + (threadIdx.x >> 6)) * kJoinCols + lane * 4;
   const uint32_t left = c < a.cols ? min(a.cols - c, 4u) : 0;
+  uint2 run = a.list[blockIdx.x];                 // read beside the count: there is room for every unit
   for (uint32_t k = blockIdx.x; k < joins; k += gridDim.x) {
-    const uint32_t u = a.list[k];
-    const uint32_t token = *G<const uint32_t>(a.keys + static_cast<uint64_t>(((u + 1) * a.unit - 1) * 4));
+    if (k != blockIdx.x) run = a.list[k];
+    const uint32_t u = run.x, token = run.y;
     v4f x = 0.0f;
     // part 0 is the beginning in unit u, part i what unit u + i begins with, as long as that is the token
     bool more = left > 0;
@@ -627,16 +598,22 @@ int64_t zero_blocks(const Zeros& z) {
 
 int enqueue_lookup(const LookupArgs& a, std::string* err) {
   if (a.n == 0) return kOk;
-  const int64_t row_groups = (a.cols + kGroup - 1) / kGroup;
-  const Lookup l = {addr(a.tokens), addr(a.table), addr(a.residual.data), addr(a.y), a.n * row_groups,
-                    a.residual.stride, static_cast<uint32_t>(row_groups), static_cast<uint32_t>(a.cols),
-                    static_cast<uint32_t>(a.vocab), a.token_bytes, a.scale};
-  const int64_t want = (l.groups + kTile - 1) / kTile;
-  const dim3 grid(static_cast<unsigned>(want < (1 << 20) ? want : 1 << 20));
+  const int64_t groups = (a.cols + kGroup - 1) / kGroup, slices = (groups + 63) / 64;
+  const Lookup l = {addr(a.tokens), addr(a.table), addr(a.residual.data), addr(a.y),
+                    static_cast<uint64_t>(a.residual.stride * dtype_size(a.dtype)), static_cast<uint32_t>(a.n),
+                    static_cast<uint32_t>(a.cols), static_cast<uint32_t>(a.vocab),
+                    static_cast<uint32_t>((groups + slices - 1) / slices), a.token_bytes, a.scale};
   hipStream_t s = static_cast<hipStream_t>(a.stream);
+  auto go = [&](auto kernel, int pack) {
+    const int64_t rows = 4 * pack * kRows, want = (a.n + rows - 1) / rows;         // rows of a workgroup
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(want < (1 << 20) ? want : 1 << 20), static_cast<unsigned>(slices)),
+                       dim3(256), 0, s, l);
+  };
   by_type(a.table_dtype, [&](auto t) {
     by_type(a.dtype, [&](auto d) {
-      hipLaunchKernelGGL((lookup_kernel<decltype(t)::value, decltype(d)::value>), grid, dim3(kThreads), 0, s, l);
+      constexpr int TD = decltype(t)::value, OD = decltype(d)::value;
+      if (a.cols % 8 != 0) groups <= 16 ? go(lookup_kernel<TD, OD, 4, true>, 4) : go(lookup_kernel<TD, OD, 1, true>, 1);
+      else groups <= 16 ? go(lookup_kernel<TD, OD, 4, false>, 4) : go(lookup_kernel<TD, OD, 1, false>, 1);
     });
   });
   HIP_OK(hipGetLastError(), "launch lookup_kernel");
@@ -693,13 +670,15 @@ int enqueue_lookup_backward(const LookupBackwardArgs& a, std::string* err) {
     }
   }
   if (a.n == 0) return kOk;
+  const int64_t groups = (a.cols + kGroup - 1) / kGroup, sums = (groups + 63) / 64;
   const Sum m = {addr(a.dy.data), addr(a.dtable), addr(words(p.keys[sorted])), addr(words(p.order[sorted])),
                  static_cast<uint64_t>(a.dy.stride * dtype_size(a.dtype)),
                  static_cast<uint64_t>(a.cols * dtype_size(a.grad_dtype)), static_cast<uint32_t>(a.n),
                  static_cast<uint32_t>(p.unit), static_cast<uint32_t>(p.units), static_cast<uint32_t>(a.cols),
-                 static_cast<uint32_t>(a.vocab), reinterpret_cast<float*>(ws + p.partials), words(p.joins),
-                 words(p.list), a.scale};
-  const dim3 grid(static_cast<unsigned>((p.units + 3) / 4), static_cast<unsigned>((a.cols + 511) / 512));
+                 static_cast<uint32_t>(a.vocab), static_cast<uint32_t>((groups + sums - 1) / sums),
+                 reinterpret_cast<float*>(ws + p.partials), words(p.joins),
+                 reinterpret_cast<uint2*>(ws + p.list), a.scale};
+  const dim3 grid(static_cast<unsigned>((p.units + 3) / 4), static_cast<unsigned>(sums));
   const int64_t slices = (a.cols + 4 * kJoinCols - 1) / (4 * kJoinCols), runs = slices < 32 ? 2048 / slices : 64;
   const dim3 join_grid(static_cast<unsigned>(runs < p.units ? runs : p.units), static_cast<unsigned>(slices));
   const bool tail = a.cols % 8 != 0;

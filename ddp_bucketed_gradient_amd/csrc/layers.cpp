@@ -206,11 +206,11 @@ LookupPlan lookup_plan(int64_t n, int64_t vocab, int64_t cols) {
     p.digit = (bits + p.passes - 1) / p.passes;
     p.tiles = (n + kSortTile - 1) / kSortTile;
   }
-  // Units of 8 places or more, so that up to 4096 waves (16 a CU) share the sum; at
+  // Units of 8 places or more, so that 1024 waves (four a CU) share the sum; at
   // most 65536 units, which bounds the partial sums.
   const int64_t waves = (cols + 64 * kGroup - 1) / (64 * kGroup);
   p.unit = 8;
-  while (p.unit < 128 && n * waves > p.unit * 4096) p.unit *= 2;
+  while (p.unit < 128 && n * waves > p.unit * 1024) p.unit *= 2;
   while (n > p.unit * 65536) p.unit *= 2;
   p.units = (n + p.unit - 1) / p.unit;
   int64_t at = 0;
@@ -226,7 +226,7 @@ LookupPlan lookup_plan(int64_t n, int64_t vocab, int64_t cols) {
   p.hist = take((p.tiles << p.digit) * 4);
   p.totals = take(int64_t(4) << p.digit);
   p.joins = take(4);
-  p.list = take(p.units * 4);
+  p.list = take(p.units * 8);
   p.partials = take(p.units > 1 ? p.units * 2 * cols * 4 : 0);
   p.bytes = at;
   return p;

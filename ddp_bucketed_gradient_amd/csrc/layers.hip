@@ -425,8 +425,8 @@ __global__ __launch_bounds__(kWeightCols * kWeightWaves) void norm_weights_kerne
 }
 
 // ---------------------------------------------------------------------------
-// Dropout, with or without a residual. A workgroup takes kDropTile groups of
-// eight elements at a time, counted row by row.
+// Dropout, with or without a residual. A workgroup takes kTile groups of eight
+// elements at a time, counted row by row.
 struct Drop {
   uint64_t x, residual, y;
   int64_t x_stride, residual_stride;   // in elements
@@ -435,20 +435,21 @@ struct Drop {
   uint32_t row_groups;                 // groups of a row, if there is more than one row
   DropSpec drop;
 };
-constexpr int kDropThreads = 256, kDropUnroll = 4, kDropTile = kDropThreads * kDropUnroll;
+constexpr int kDropThreads = 256;
 
-template <int D, bool FLAT>
+template <int D, bool FLAT, int UNROLL>
 __global__ __launch_bounds__(kDropThreads) void dropout_kernel(Drop a) {
   typedef typename Of<D>::one one;
+  constexpr int kTile = kDropThreads * UNROLL;
   const uint64_t offset = offset_of(a.drop);
-  for (int64_t tile = static_cast<int64_t>(blockIdx.x) * kDropTile; tile < a.groups;
-       tile += static_cast<int64_t>(gridDim.x) * kDropTile) {
-    int64_t row[kDropUnroll], c[kDropUnroll];
-    v8f x[kDropUnroll], r[kDropUnroll];
+  for (int64_t tile = static_cast<int64_t>(blockIdx.x) * kTile; tile < a.groups;
+       tile += static_cast<int64_t>(gridDim.x) * kTile) {
+    int64_t row[UNROLL], c[UNROLL];
+    v8f x[UNROLL], r[UNROLL];
     const int64_t row0 = FLAT ? 0 : tile / a.row_groups;
     const uint32_t rest = FLAT ? 0 : static_cast<uint32_t>(tile - row0 * a.row_groups);
 #pragma unroll
-    for (int u = 0; u < kDropUnroll; ++u) {
+    for (int u = 0; u < UNROLL; ++u) {
       const uint32_t i = u * kDropThreads + threadIdx.x;
       if (FLAT) {
         row[u] = 0;
@@ -465,7 +466,7 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(Drop a) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < kDropUnroll; ++u) {
+    for (int u = 0; u < UNROLL; ++u) {
       if (tile + u * kDropThreads + threadIdx.x >= a.groups) continue;
       const int64_t first = row[u] * a.cols + c[u];
       v8f z = x[u];
@@ -579,11 +580,17 @@ class HipLayersDevice final : public LayersDevice {
     const int64_t row_groups = (d.cols + kGroup - 1) / kGroup;
     d.groups = flat ? row_groups : row_groups * a.rows;
     d.row_groups = flat ? 1 : static_cast<uint32_t>(row_groups);
-    const unsigned blocks = grid_of((d.groups + kDropTile - 1) / kDropTile, 1 << 20);
     hipStream_t s = static_cast<hipStream_t>(a.stream);
+    // four groups to a lane where that leaves eight workgroups a CU, else one
+    const bool many = d.groups >= int64_t(2048) * 4 * kDropThreads;
+    const int64_t tile = many ? 4 * kDropThreads : kDropThreads;
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(grid_of((d.groups + tile - 1) / tile, 1 << 20)), dim3(kDropThreads), 0, s, d);
+    };
     by_type(a.dtype, [&](auto t) {
-      if (flat) hipLaunchKernelGGL((dropout_kernel<decltype(t)::value, true>), dim3(blocks), dim3(kDropThreads), 0, s, d);
-      else hipLaunchKernelGGL((dropout_kernel<decltype(t)::value, false>), dim3(blocks), dim3(kDropThreads), 0, s, d);
+      constexpr int D = decltype(t)::value;
+      if (flat) many ? go(dropout_kernel<D, true, 4>) : go(dropout_kernel<D, true, 1>);
+      else many ? go(dropout_kernel<D, false, 4>) : go(dropout_kernel<D, false, 1>);
     });
     HIP_OK(hipGetLastError(), "launch dropout_kernel");
     return kOk;

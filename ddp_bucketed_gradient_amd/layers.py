@@ -18,6 +18,18 @@ from . import _abi
 from .optim import _code
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported with the first call."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 class Drop:
     """Which elements a dropout keeps: a function of the seed, the offset and an
     element's index, so that nothing is stored for the backward pass, which
@@ -111,21 +123,26 @@ def _vector(t, what: str, n: int, device, dtype=None):
 
 def _call(device, f, *args):
     """f(*args, stream) on the current stream of ``device``."""
-    import torch
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    torch = _t()
+    i = device.index
+    stream = torch._C._cuda_getCurrentRawStream(i)   # current_stream(device).cuda_stream without its Stream object
+    if torch.cuda.current_device() == i:
         return f(*args, stream)
     with torch.cuda.device(device):
         return f(*args, stream)
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape, type and device."""
+    return _t().empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _wrote(*ts):
     """The gradients were written in place, through their addresses: autograd
     counts writes by tensor."""
-    import torch
     for t in ts:
         if t is not None:
-            torch.autograd.graph.increment_version(t)
+            _t().autograd.graph.increment_version(t)
 
 
 def _lib(lib):
@@ -134,12 +151,14 @@ def _lib(lib):
 
 def dropout(x, drop: Drop, residual=None, lib: Optional[_abi.Lib] = None):
     """``x`` with a share of its elements dropped and the others scaled, plus
-    ``residual``. Contiguous, of x's type (fp32, bf16 or fp16)."""
-    import torch
+    ``residual``. Contiguous, of x's type (fp32, bf16 or fp16); x itself where
+    nothing is dropped or added."""
     code = _code(x.dtype, "x")
     rows, cols, stride = _rows(x, "x")
     rs = 0 if residual is None else _rows(residual, "residual", x)[2]
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if residual is None and not drop.active and x.is_contiguous():
+        return x
+    y = _like(x)
     _call(x.device, _lib(lib).dropout, rows, cols, code, x.data_ptr(), stride,
           0 if residual is None else residual.data_ptr(), rs, drop._on(x.device), y.data_ptr())
     return y
@@ -154,16 +173,15 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, drop
                lib: Optional[_abi.Lib] = None) -> Normed:
     """Layer norm over the last dimension of ``h = residual + dropout(x)``, in
     one pass. ``weight`` and ``bias``: one type, which may differ from x's."""
-    import torch
     code, dev = _code(x.dtype, "x"), x.device
     rows, cols, stride = _rows(x, "x")
     rs = 0 if residual is None else _rows(residual, "residual", x)[2]
     wt = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
     w, b = _vector(weight, "weight", cols, dev, wt), _vector(bias, "bias", cols, dev, wt)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = _like(x)
     fused = residual is not None or (drop is not None and drop.active)
-    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if fused else x
-    stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=dev)
+    h = _like(x) if fused else x
+    stats = x.new_empty(x.shape[:-1] + (2,), dtype=_t().float32)
     _call(dev, _lib(lib).layer_norm, rows, cols, code, x.data_ptr(), stride,
           0 if residual is None else residual.data_ptr(), rs, None if drop is None else drop._on(dev), w, b,
           _code(wt, "weight and bias"), eps, y.data_ptr(), h.data_ptr() if fused else 0, stats.data_ptr())
@@ -178,7 +196,7 @@ def layer_norm_backward(dy, h, stats, weight=None, dweight=None, dbias=None, gra
     wanted; one type): written, or with ``accumulate`` added to. ``grad_h``: a
     gradient that reaches h from elsewhere, as where h itself goes on as the
     next residual."""
-    import torch
+    torch = _t()
     code, dev = _code(dy.dtype, "dy"), dy.device
     rows, cols, stride = _rows(dy, "dy")
     hs = _rows(h, "h", dy)[2]
@@ -191,9 +209,9 @@ def layer_norm_backward(dy, h, stats, weight=None, dweight=None, dbias=None, gra
     ws = None
     if dw or db:
         ws = torch.empty(lib.layer_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
-    dh = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    dh = _like(dy)
     dropped = drop is not None and drop.active
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dev) if dropped else dh
+    dx = _like(dy) if dropped else dh
     _call(dev, lib.layer_norm_backward, rows, cols, code, dy.data_ptr(), stride, h.data_ptr(), hs, st,
           0 if grad_h is None else grad_h.data_ptr(), gs, drop._on(dev) if dropped else None, w,
           code if weight is None else _code(weight.dtype, "weight"), dh.data_ptr(), dx.data_ptr() if dropped else 0,
@@ -205,7 +223,7 @@ def layer_norm_backward(dy, h, stats, weight=None, dweight=None, dbias=None, gra
 
 def _tokens(tokens, device):
     """(count, address, bytes) of a tensor of tokens."""
-    import torch
+    torch = _t()
     size = {torch.int64: 8, torch.int32: 4}.get(tokens.dtype)
     if size is None or not tokens.is_cuda or tokens.device != device or not tokens.is_contiguous():
         raise ValueError(f"tokens must be a contiguous int64 or int32 CUDA tensor on {device}")
@@ -221,13 +239,12 @@ def _table(t, what: str):
 def embedding(tokens, table, scale: float = 1.0, residual=None, dtype=None, lib: Optional[_abi.Lib] = None):
     """``scale * table[tokens] + residual``, of the table's type or ``dtype``. A
     token outside of the table gives a row of zeros."""
-    import torch
     vocab, cols, tc = _table(table, "table")
     dev = table.device
     n, at, size = _tokens(tokens, dev)
     dtype = table.dtype if dtype is None else dtype
     code = _code(dtype, "dtype")
-    y = torch.empty(tokens.shape + (cols,), dtype=dtype, device=dev)
+    y = table.new_empty(tokens.shape + (cols,), dtype=dtype)
     rs = 0 if residual is None else _rows(residual, "residual", y)[2]
     _call(dev, _lib(lib).embedding, n, at, size, vocab, cols, table.data_ptr(), tc, scale,
           0 if residual is None else residual.data_ptr(), rs, y.data_ptr(), code)
@@ -240,7 +257,7 @@ def embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bool 
     ``dtable`` becomes ``scale`` times the sum of dy over the places of token v,
     in their order; with ``accumulate`` that is added to it. Tokens outside of the
     table are left out. Returns dtable."""
-    import torch
+    torch = _t()
     vocab, cols, gc = _table(dtable, "dtable")
     dev = dtable.device
     n, at, size = _tokens(tokens, dev)

@@ -153,7 +153,7 @@ def test_workspaces_stay_in_bounds(lib):
         # keys and order twice; histograms of at most 1024 counters for 4096 keys; two partial sums for each unit of
         # 8 or more places, of which there are at most 65536
         units = min(n // 8 + 1, 65536)
-        assert 16 * n <= b <= 16 * n + (n // 4096 + 1) * 4096 + units * (8 * cols + 4) + 32768 and b % 256 == 0
+        assert 16 * n <= b <= 16 * n + (n // 4096 + 1) * 4096 + units * (8 * cols + 8) + 32768 and b % 256 == 0
 
 
 def test_null_results(lib):

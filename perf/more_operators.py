@@ -245,11 +245,13 @@ def _run_own(s):
     if c["op"] == "lookup_grad":
         D.embedding_backward(s["dy"], s["tokens"], s["dtable"], SCALE, accumulate=c["add"])
         return s["dtable"]
-    t = DTYPES[c["t"]]
-    words = D.embedding(s["tokens"], s["table"], SCALE, dtype=t)
-    n = D.layer_norm(D.embedding(s["places"], s["where"], residual=words, dtype=t), s["w"], s["b"], EPS)
-    y = D.dropout(n.y, s["drop"])
-    dh = D.layer_norm_backward(D.dropout_backward(s["dy"], s["drop"]), n.h, n.stats, s["w"], s["dw"], s["db"]).dh
+    # in fp32 throughout, as mixed precision keeps its norms: the parameters' gradients are fp32
+    f = torch.float32
+    words = D.embedding(s["tokens"], s["table"], SCALE, dtype=f)
+    n = D.layer_norm(D.embedding(s["places"], s["where"], residual=words, dtype=f), s["w"], s["b"], EPS)
+    y = D.dropout(n.y, s["drop"]).to(DTYPES[c["t"]])
+    dy = D.dropout_backward(s["dy"].float(), s["drop"])
+    dh = D.layer_norm_backward(dy, n.h, n.stats, s["w"], s["dw"], s["db"]).dh
     D.embedding_backward(dh, s["tokens"], s["dtable"], SCALE)
     D.embedding_backward(dh, s["places"], s["dwhere"])
     return {"y": y, "dtable": s["dtable"], "dwhere": s["dwhere"], "dw": s["dw"], "db": s["db"]}

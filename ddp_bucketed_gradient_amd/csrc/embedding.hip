@@ -20,25 +20,24 @@ __device__ __forceinline__ uint32_t token_at(uint64_t tokens, int32_t bytes, int
 struct Lookup {
   uint64_t tokens, table, residual, y;
   uint64_t residual_row;        // bytes from row to row
-  uint32_t n, cols, vocab, slice;
+  uint32_t n, cols, vocab, slice, shift;
   int32_t token_bytes;
   float scale;
 };
 
 // A wave takes kRows rows of one slice, 64 groups of eight columns or less, so
-// that tokens and row addresses are uniform. Rows of 16 groups and less share a
-// wave: PACK of them, side by side.
+// that tokens and row addresses are uniform. Rows of 32 groups and less share a
+// wave, a power of two of lanes each (PACKED).
 constexpr int kRows = 4;
-template <int TD, int D, int PACK, bool TAIL>
+template <int TD, int D, bool PACKED, int EDGE>
 __global__ __launch_bounds__(256) void lookup_kernel(Lookup a) {
   constexpr uint32_t size = sizeof(typename Of<D>::one), table_size = sizeof(typename Of<TD>::one);
-  constexpr uint32_t LANES = 64 / PACK;
-  const uint32_t lane = threadIdx.x % LANES;
-  const uint32_t c = (blockIdx.y * a.slice + lane) * 8;
-  const int left = lane >= a.slice || c >= a.cols ? 0 : TAIL ? static_cast<int>(min(a.cols - c, 8u)) : 8;
-  if (left <= 0) return;
-  const uint32_t part = PACK > 1 ? threadIdx.x / LANES : __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
-  for (uint32_t first = (blockIdx.x * (256 / LANES) + part) * kRows; first < a.n; first += gridDim.x * (256 / LANES) * kRows) {
+  const uint32_t lane = PACKED ? threadIdx.x & ((1u << a.shift) - 1) : threadIdx.x & 63;
+  const uint32_t part = PACKED ? threadIdx.x >> a.shift : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t parts = PACKED ? 256u >> a.shift : 4;
+  const Group g = group_at<EDGE>(a.cols, (blockIdx.y * a.slice + lane) * 8);
+  if (g.left <= 0 || lane >= a.slice) return;
+  for (uint32_t first = (blockIdx.x * parts + part) * kRows; first < a.n; first += gridDim.x * parts * kRows) {
     uint32_t t[kRows];
     Raw<TD> x[kRows];
     Raw<D> r[kRows];
@@ -49,8 +48,8 @@ __global__ __launch_bounds__(256) void lookup_kernel(Lookup a) {
     for (int k = 0; k < kRows; ++k) {
       x[k] = Raw<TD>{};
       r[k] = Raw<D>{};
-      if (t[k] < a.vocab) x[k] = load_raw<TD, TAIL>(a.table + static_cast<uint64_t>(t[k]) * a.cols * table_size + c * table_size, left);
-      if (a.residual != 0 && first + k < a.n) r[k] = load_raw<D, TAIL>(a.residual + (first + k) * a.residual_row + c * size, left);
+      if (t[k] < a.vocab) x[k] = load_raw<TD, EDGE>(a.table + static_cast<uint64_t>(t[k]) * a.cols * table_size + g.c * table_size, g.left);
+      if (a.residual != 0 && first + k < a.n) r[k] = load_raw<D, EDGE>(a.residual + (first + k) * a.residual_row + g.c * size, g.left);
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -58,7 +57,7 @@ __global__ __launch_bounds__(256) void lookup_kernel(Lookup a) {
       v8f y = 0.0f;
       if (t[k] < a.vocab) y = widen<TD>(x[k]) * a.scale;
       if (a.residual != 0) y = y + widen<D>(r[k]);
-      store8<D, TAIL>(a.y + static_cast<uint64_t>(first + k) * a.cols * size + c * size, left, y);
+      store8<D, EDGE>(a.y + static_cast<uint64_t>(first + k) * a.cols * size + g.c * size, g.left, y);
     }
   }
 }
@@ -413,19 +412,18 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t x, int i) {
 // A wave sums eight columns a lane of one unit. The keys and places of 64 sorted
 // places lie in its lanes, so that the run ends are a mask and everything but
 // the rows themselves is uniform. The rows of kAhead places are loaded together,
-// with what stands in the table where the sums are added to that. TAIL: rows
-// that do not end on a multiple of eight. The code of each variant is kept short
-// (one wave runs most of it once): with the tails and 64-bit indexes in one
-// kernel of 11 KB half of the waves' time went into fetching it.
-template <int D, int GD, bool ADD, bool TAIL>
+// with what stands in the table where the sums are added to that.
+template <int D, int GD, bool ADD, int EDGE>
 __global__ __launch_bounds__(256) void sum_kernel(Sum a) {
   typedef typename Of<D>::one one;
   typedef typename Of<GD>::one grad_one;
   constexpr int kAhead = 8;
   const uint32_t u = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (u >= a.units) return;
-  const uint32_t lane = threadIdx.x & 63, c = (blockIdx.y * a.slice + lane) * 8;
-  const int left = c >= a.cols || lane >= a.slice ? 0 : TAIL ? static_cast<int>(min(a.cols - c, 8u)) : 8;
+  const uint32_t lane = threadIdx.x & 63;
+  const Group g = group_at<EDGE>(a.cols, lane < a.slice ? (blockIdx.y * a.slice + lane) * 8 : a.cols);
+  const uint32_t c = g.c;
+  const int left = g.left;
   const uint32_t s = u * a.unit, e = min(s + a.unit, a.n), e2 = min(e + a.unit, a.n);
   const uint32_t first = key_at(a, s), last = key_at(a, e - 1);
   const uint32_t before = key_at(a, s > 0 ? s - 1 : 0), unit_before = key_at(a, s > 0 ? s - a.unit : 0);
@@ -467,10 +465,10 @@ __global__ __launch_bounds__(256) void sum_kernel(Sum a) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           const int at = min(j + k, to - 1);
-          rows[k] = load_raw<D, TAIL>(a.dy + lane_of(place, at) * a.dy_row + c * static_cast<uint32_t>(sizeof(one)), left);
+          rows[k] = load_raw<D, EDGE>(a.dy + lane_of(place, at) * a.dy_row + c * static_cast<uint32_t>(sizeof(one)), left);
           if constexpr (ADD) {
             if (j + k < to && (ends >> at & 1))
-              old[k] = load_raw<GD, TAIL>(a.dtable + lane_of(key, at) * a.table_row + c * static_cast<uint32_t>(sizeof(grad_one)), left);
+              old[k] = load_raw<GD, EDGE>(a.dtable + lane_of(key, at) * a.table_row + c * static_cast<uint32_t>(sizeof(grad_one)), left);
           }
         }
 #pragma unroll
@@ -479,11 +477,11 @@ __global__ __launch_bounds__(256) void sum_kernel(Sum a) {
           x = x + widen<D>(rows[k]);
           if ((ends >> (j + k) & 1) == 0) continue;
           if (open_left) {
-            store8<kF32, TAIL>(partial, left, x);
+            store8<kF32, EDGE>(partial, left, x);
           } else {
             x = x * a.scale;
             if constexpr (ADD) x = x + widen<GD>(old[k]);
-            store8<GD, TAIL>(a.dtable + lane_of(key, j + k) * a.table_row + c * static_cast<uint32_t>(sizeof(grad_one)), left, x);
+            store8<GD, EDGE>(a.dtable + lane_of(key, j + k) * a.table_row + c * static_cast<uint32_t>(sizeof(grad_one)), left, x);
           }
           open_left = false;
           x = 0.0f;
@@ -494,8 +492,8 @@ __global__ __launch_bounds__(256) void sum_kernel(Sum a) {
     open_left = open_left && ends == 0;               // the same in lanes without columns
   }
   if (!pending) return;
-  if (left > 0) store8<kF32, TAIL>(partial + (open_left ? 0 : static_cast<uint64_t>(a.cols) * 4), left, x);
-  if (!open_left && c == 0) a.list[atomicAdd(a.joins, 1u)] = make_uint2(u, last);
+  if (left > 0) store8<kF32, EDGE>(partial + (open_left ? 0 : static_cast<uint64_t>(a.cols) * 4), left, x);
+  if (!open_left && blockIdx.y == 0 && lane == 0) a.list[atomicAdd(a.joins, 1u)] = make_uint2(u, last);
 }
 
 // The runs that cover whole units: 16 columns to a wave, four to a lane, and 16
@@ -599,21 +597,22 @@ int64_t zero_blocks(const Zeros& z) {
 int enqueue_lookup(const LookupArgs& a, std::string* err) {
   if (a.n == 0) return kOk;
   const int64_t groups = (a.cols + kGroup - 1) / kGroup, slices = (groups + 63) / 64;
+  uint32_t shift = 0;                              // lanes of a row
+  while ((1 << shift) < groups && shift < 6) ++shift;
   const Lookup l = {addr(a.tokens), addr(a.table), addr(a.residual.data), addr(a.y),
                     static_cast<uint64_t>(a.residual.stride * dtype_size(a.dtype)), static_cast<uint32_t>(a.n),
                     static_cast<uint32_t>(a.cols), static_cast<uint32_t>(a.vocab),
-                    static_cast<uint32_t>((groups + slices - 1) / slices), a.token_bytes, a.scale};
+                    static_cast<uint32_t>((groups + slices - 1) / slices), shift, a.token_bytes, a.scale};
   hipStream_t s = static_cast<hipStream_t>(a.stream);
-  auto go = [&](auto kernel, int pack) {
-    const int64_t rows = 4 * pack * kRows, want = (a.n + rows - 1) / rows;         // rows of a workgroup
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(want < (1 << 20) ? want : 1 << 20), static_cast<unsigned>(slices)),
-                       dim3(256), 0, s, l);
-  };
+  const int64_t rows = (256 >> shift) * kRows, want = (a.n + rows - 1) / rows;         // rows of a workgroup
+  const dim3 grid(static_cast<unsigned>(want < (1 << 20) ? want : 1 << 20), static_cast<unsigned>(slices));
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, l); };
   by_type(a.table_dtype, [&](auto t) {
     by_type(a.dtype, [&](auto d) {
       constexpr int TD = decltype(t)::value, OD = decltype(d)::value;
-      if (a.cols % 8 != 0) groups <= 16 ? go(lookup_kernel<TD, OD, 4, true>, 4) : go(lookup_kernel<TD, OD, 1, true>, 1);
-      else groups <= 16 ? go(lookup_kernel<TD, OD, 4, false>, 4) : go(lookup_kernel<TD, OD, 1, false>, 1);
+      if (a.cols < 8) go(lookup_kernel<TD, OD, true, kSmall>);
+      else if (a.cols % 8 == 0) shift < 6 ? go(lookup_kernel<TD, OD, true, kWhole>) : go(lookup_kernel<TD, OD, false, kWhole>);
+      else shift < 6 ? go(lookup_kernel<TD, OD, true, kShifted>) : go(lookup_kernel<TD, OD, false, kShifted>);
     });
   });
   HIP_OK(hipGetLastError(), "launch lookup_kernel");
@@ -670,25 +669,34 @@ int enqueue_lookup_backward(const LookupBackwardArgs& a, std::string* err) {
     }
   }
   if (a.n == 0) return kOk;
-  const int64_t groups = (a.cols + kGroup - 1) / kGroup, sums = (groups + 63) / 64;
+  // Slices of the columns, a wave each. A last group that is shifted has the lane
+  // before it in its own wave, which reads what both add to before either writes it.
+  const int64_t groups = (a.cols + kGroup - 1) / kGroup;
+  int64_t sums = (groups + 63) / 64;
+  auto slice = [&] { return (groups + sums - 1) / sums; };
+  while (sums > 1 && groups % slice() == 1) ++sums;
   const Sum m = {addr(a.dy.data), addr(a.dtable), addr(words(p.keys[sorted])), addr(words(p.order[sorted])),
                  static_cast<uint64_t>(a.dy.stride * dtype_size(a.dtype)),
                  static_cast<uint64_t>(a.cols * dtype_size(a.grad_dtype)), static_cast<uint32_t>(a.n),
                  static_cast<uint32_t>(p.unit), static_cast<uint32_t>(p.units), static_cast<uint32_t>(a.cols),
-                 static_cast<uint32_t>(a.vocab), static_cast<uint32_t>((groups + sums - 1) / sums),
+                 static_cast<uint32_t>(a.vocab), static_cast<uint32_t>(slice()),
                  reinterpret_cast<float*>(ws + p.partials), words(p.joins),
                  reinterpret_cast<uint2*>(ws + p.list), a.scale};
   const dim3 grid(static_cast<unsigned>((p.units + 3) / 4), static_cast<unsigned>(sums));
   const int64_t slices = (a.cols + 4 * kJoinCols - 1) / (4 * kJoinCols), runs = slices < 32 ? 2048 / slices : 64;
   const dim3 join_grid(static_cast<unsigned>(runs < p.units ? runs : p.units), static_cast<unsigned>(slices));
-  const bool tail = a.cols % 8 != 0;
   by_type(a.grad_dtype, [&](auto g) {
     constexpr int GD = decltype(g)::value;
     by_type(a.dtype, [&](auto d) {
       constexpr int TD = decltype(d)::value;
       auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, m); };
-      if (a.accumulate) tail ? go(sum_kernel<TD, GD, true, true>) : go(sum_kernel<TD, GD, true, false>);
-      else tail ? go(sum_kernel<TD, GD, false, true>) : go(sum_kernel<TD, GD, false, false>);
+      auto pick = [&](auto add) {
+        constexpr bool ADD = decltype(add)::value;
+        if (a.cols < 8) go(sum_kernel<TD, GD, ADD, kSmall>);
+        else a.cols % 8 == 0 ? go(sum_kernel<TD, GD, ADD, kWhole>) : go(sum_kernel<TD, GD, ADD, kShifted>);
+      };
+      if (a.accumulate) pick(std::true_type());
+      else pick(std::false_type());
     });
     if (p.units <= 1) return;
     if (a.accumulate) hipLaunchKernelGGL((join_kernel<GD, true>), join_grid, dim3(256), 0, s, m);

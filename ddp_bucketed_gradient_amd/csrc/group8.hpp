@@ -34,19 +34,45 @@ __device__ __forceinline__ __attribute__((address_space(1))) T* G(uint64_t a) {
   return (__attribute__((address_space(1))) T*)a;
 }
 
-// Eight elements at the address `a`, of which `left` exist (none or less: none);
-// the others are 0. Vectors are only assumed to be aligned like their
-// element: gfx950's memory instructions take any such address, and odd row
-// lengths and bucket views make them.
+// How rows end. Rows of a multiple of eight consist of whole groups. Where they
+// do not, the last group begins eight elements before the end: its lane reads
+// and writes whole vectors too, some of them a second time with the same values
+// (one element at a time took up to three times as long). Rows of less than eight
+// elements are one group that is read and written element by element.
+enum Edge { kWhole = 0, kShifted = 1, kSmall = 2 };
+
+struct Group {
+  uint32_t c;      // first column
+  int left;        // columns that exist, 0 where the lane has none
+  int skip;        // of these, how many the lane before has too (kShifted)
+};
+
+template <int EDGE>
+__device__ __forceinline__ Group group_at(uint32_t cols, uint32_t c) {
+  if (c >= cols) return {0, 0, 0};
+  if (EDGE == kSmall) return {c, static_cast<int>(min(cols - c, 8u)), 0};
+  if (EDGE == kShifted && cols - c < 8) return {cols - 8, 8, static_cast<int>(c + 8 - cols)};
+  return {c, 8, 0};
+}
+
+// Whether element j of a group is its lane's own.
+template <int EDGE>
+__device__ __forceinline__ bool own(const Group& g, int j) {
+  return EDGE == kWhole || (EDGE == kShifted ? j >= g.skip : j < g.left);
+}
+
+// Eight elements at the address `a` as they lie there, or `left` of them (kSmall).
+// Vectors are only assumed to be aligned like their element: gfx950's memory
+// instructions take any such address, and odd row lengths and bucket views make
+// them.
 template <int D>
 using Raw = typename Of<D>::one __attribute__((ext_vector_type(8)));
 
-// (TAIL false: the caller knows that all eight exist.)
-template <int D, bool TAIL = true>
-__device__ __forceinline__ Raw<D> load_raw(uint64_t a, int64_t left) {
+template <int D, int EDGE>
+__device__ __forceinline__ Raw<D> load_raw(uint64_t a, int left) {
   typedef typename Of<D>::one one;
   typedef Raw<D> any __attribute__((aligned(sizeof(one))));
-  if (!TAIL || left >= 8) return *G<const any>(a);
+  if (EDGE != kSmall || left >= 8) return *G<const any>(a);
   Raw<D> x = {};
 #pragma unroll
   for (int j = 0; j < 7; ++j)
@@ -57,15 +83,12 @@ __device__ __forceinline__ Raw<D> load_raw(uint64_t a, int64_t left) {
 template <int D>
 __device__ __forceinline__ v8f widen(Raw<D> x) { return __builtin_convertvector(x, v8f); }
 
-template <int D>
-__device__ __forceinline__ v8f load8(uint64_t a, int64_t left) { return widen<D>(load_raw<D>(a, left)); }
-
-// The same from element c of an array whose type is known when the kernel runs.
-template <bool TAIL>
-__device__ __forceinline__ v8f load8(int dtype, uint64_t a, uint32_t c, int64_t left) {
-  if (dtype == kF32) return widen<kF32>(load_raw<kF32, TAIL>(a + c * 4u, left));
-  if (dtype == kBF16) return widen<kBF16>(load_raw<kBF16, TAIL>(a + c * 2u, left));
-  return widen<kF16>(load_raw<kF16, TAIL>(a + c * 2u, left));
+// A group of an array whose type is known when the kernel runs, as fp32.
+template <int EDGE>
+__device__ __forceinline__ v8f load8(int dtype, uint64_t a, const Group& g) {
+  if (dtype == kF32) return widen<kF32>(load_raw<kF32, EDGE>(a + g.c * 4u, g.left));
+  if (dtype == kBF16) return widen<kBF16>(load_raw<kBF16, EDGE>(a + g.c * 2u, g.left));
+  return widen<kF16>(load_raw<kF16, EDGE>(a + g.c * 2u, g.left));
 }
 
 // Rounds to nearest even where D has 16 bits: the one rounding that an output
@@ -73,13 +96,13 @@ __device__ __forceinline__ v8f load8(int dtype, uint64_t a, uint32_t c, int64_t 
 // forward 23.5 us instead of 25.5, backward 28.5 instead of 32.8); fp32's are
 // not, whose halves of 16 bytes would reach memory as parts of lines (a backward
 // pass of 8192 x 8192: 209 us instead of 203).
-template <int D, bool TAIL = true>
-__device__ __forceinline__ void store8(uint64_t a, int64_t left, v8f x) {
+template <int D, int EDGE>
+__device__ __forceinline__ void store8(uint64_t a, int left, v8f x) {
   typedef typename Of<D>::one one;
   typedef one raw __attribute__((ext_vector_type(8)));
   typedef raw any __attribute__((aligned(sizeof(one))));
   const raw y = __builtin_convertvector(x, raw);
-  if (!TAIL || left >= 8) {
+  if (EDGE != kSmall || left >= 8) {
     if constexpr (sizeof(one) == 2) __builtin_nontemporal_store(static_cast<any>(y), G<any>(a));
     else *G<any>(a) = y;
     return;

@@ -61,7 +61,6 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float* lds) {
   }
 }
 
-__device__ __forceinline__ float total(v8f x) { return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])); }
 __device__ __forceinline__ v8f fma8(v8f a, v8f b, v8f c) { return __builtin_elementwise_fma(a, b, c); }
 
 // The statistics of a row: mean, 1 / deviation.
@@ -94,30 +93,34 @@ __device__ __forceinline__ uint32_t row_of_lane() {
   return LANES >= 64 ? __builtin_amdgcn_readfirstlane(r) : r;
 }
 
-// Columns of the group at c that exist: TAIL false where rows are a multiple of eight.
-template <bool TAIL>
-__device__ __forceinline__ int left_of(uint32_t cols, uint32_t c) {
-  return c >= cols ? 0 : TAIL ? static_cast<int>(min(cols - c, 8u)) : 8;
-}
-
-// z of elements c .. c+7 of a row: what the norm is taken of, in fp32.
-template <int D, bool FUSED, bool TAIL>
-__device__ __forceinline__ v8f input8(const Forward& a, uint32_t row, uint32_t c, int left, uint64_t offset) {
+// z of a group of a row: what the norm is taken of, in fp32.
+template <int D, bool FUSED, int EDGE>
+__device__ __forceinline__ v8f input8(const Forward& a, uint32_t row, const Group& g, uint64_t offset) {
   constexpr uint32_t size = sizeof(typename Of<D>::one);
   Raw<D> r = {};
-  if (FUSED && a.residual != 0) r = load_raw<D, TAIL>(a.residual + row * a.residual_row + c * size, left);
-  v8f z = widen<D>(load_raw<D, TAIL>(a.x + row * a.x_row + c * size, left));
+  if (FUSED && a.residual != 0) r = load_raw<D, EDGE>(a.residual + row * a.residual_row + g.c * size, g.left);
+  v8f z = widen<D>(load_raw<D, EDGE>(a.x + row * a.x_row + g.c * size, g.left));
   if constexpr (FUSED) {
-    if (a.drop.limit != 0) z = drop8(z, static_cast<uint64_t>(row) * a.cols + c, offset, a.drop);
+    if (a.drop.limit != 0) z = drop8(z, static_cast<uint64_t>(row) * a.cols + g.c, offset, a.drop);
     if (a.residual != 0) z = z + widen<D>(r);
   }
   return z;
 }
 
+// The sum of a group's own elements.
+template <int EDGE>
+__device__ __forceinline__ float total(v8f x, const Group& g) {
+  if (EDGE == kShifted) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j) x[j] = own<EDGE>(g, j) ? x[j] : 0.0f;
+  }
+  return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+}
+
 // y = (z - mean) rstd w + b. The statistics are those of z in fp32 (the mean
 // first, then the squares of what is left: no cancellation); h, z as the
 // backward pass reads it, is rounded to the type of x for its store only.
-template <int D, int LANES, int K, bool FUSED, bool TAIL>
+template <int D, int LANES, int K, bool FUSED, int EDGE>
 __global__ __launch_bounds__(norm_threads(LANES)) void norm_forward_kernel(Forward a) {
   constexpr uint32_t size = sizeof(typename Of<D>::one);
   constexpr uint32_t ROWS = norm_threads(LANES) / LANES;
@@ -126,15 +129,14 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_forward_kernel(Forwa
   const uint64_t offset = FUSED ? offset_of(a.drop) : 0;
   const float inverse = 1.0f / static_cast<float>(a.cols);
   v8f w[K], b[K];
-  int left[K];
+  Group g[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const uint32_t c = (lane + k * LANES) * 8;
-    left[k] = left_of<TAIL>(a.cols, c);
+    g[k] = group_at<EDGE>(a.cols, (lane + k * LANES) * 8);
     w[k] = 1.0f;
     b[k] = 0.0f;
-    if (left[k] > 0 && a.weight != 0) w[k] = load8<TAIL>(a.weight_dtype, a.weight, c, left[k]);
-    if (left[k] > 0 && a.bias != 0) b[k] = load8<TAIL>(a.weight_dtype, a.bias, c, left[k]);
+    if (g[k].left > 0 && a.weight != 0) w[k] = load8<EDGE>(a.weight_dtype, a.weight, g[k]);
+    if (g[k].left > 0 && a.bias != 0) b[k] = load8<EDGE>(a.weight_dtype, a.bias, g[k]);
   }
   for (uint32_t row = blockIdx.x * ROWS + row_of_lane<LANES>(); row < a.rows; row += gridDim.x * ROWS) {
     v8f z[K];
@@ -142,22 +144,22 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_forward_kernel(Forwa
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       z[k] = 0.0f;
-      if (left[k] > 0) z[k] = input8<D, FUSED, TAIL>(a, row, (lane + k * LANES) * 8, left[k], offset);
+      if (g[k].left > 0) z[k] = input8<D, FUSED, EDGE>(a, row, g[k], offset);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[0] += total(z[k]);
+    for (int k = 0; k < K; ++k) s[0] += total<EDGE>(z[k], g[k]);
     row_sum<LANES>(s, lds[0]);
     const float mean = s[0] * inverse;
     float q[1] = {0.0f};
     const uint64_t at = static_cast<uint64_t>(row) * a.cols * size;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (left[k] <= 0) continue;
-      if (FUSED && a.h != 0) store8<D, TAIL>(a.h + at + (lane + k * LANES) * 8 * size, left[k], z[k]);
+      if (g[k].left <= 0) continue;
+      if (FUSED && a.h != 0) store8<D, EDGE>(a.h + at + g[k].c * size, g[k].left, z[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = z[k][j] - mean;
-        q[0] = __builtin_fmaf(!TAIL || j < left[k] ? d : 0.0f, d, q[0]);
+        q[0] = __builtin_fmaf(own<EDGE>(g[k], j) ? d : 0.0f, d, q[0]);
         z[k][j] = d;
       }
     }
@@ -165,7 +167,7 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_forward_kernel(Forwa
     const float rstd = 1.0f / __builtin_sqrtf(q[0] * inverse + a.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (left[k] > 0) store8<D, TAIL>(a.y + at + (lane + k * LANES) * 8 * size, left[k], fma8(z[k] * rstd, w[k], b[k]));
+      if (g[k].left > 0) store8<D, EDGE>(a.y + at + g[k].c * size, g[k].left, fma8(z[k] * rstd, w[k], b[k]));
     if (lane == 0) put_stats(a.stats, row, mean, rstd);
   }
 }
@@ -175,36 +177,38 @@ constexpr int kLong = 1024;   // threads for a row that no shape holds in regist
 template <int D, bool FUSED>
 __global__ __launch_bounds__(kLong) void norm_forward_long_kernel(Forward a) {
   constexpr uint32_t size = sizeof(typename Of<D>::one);
+  constexpr int EDGE = kShifted;
   __shared__ float lds[2][kLong / 64 * 2];
   const uint64_t offset = FUSED ? offset_of(a.drop) : 0;
   const float inverse = 1.0f / static_cast<float>(a.cols);
-  auto z8 = [&](uint32_t row, uint32_t c) {
-    return input8<D, FUSED, true>(a, row, c, left_of<true>(a.cols, c), offset);
-  };
   for (uint32_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     float s[1] = {0.0f}, q[1] = {0.0f};
     const uint64_t at = static_cast<uint64_t>(row) * a.cols * size;
-    for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) s[0] += total(z8(row, c));
+    for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) {
+      const Group g = group_at<EDGE>(a.cols, c);
+      s[0] += total<EDGE>(input8<D, FUSED, EDGE>(a, row, g, offset), g);
+    }
     row_sum<kLong>(s, lds[0]);
     const float mean = s[0] * inverse;
     for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) {
-      const v8f z = z8(row, c);
-      const int left = left_of<true>(a.cols, c);
-      if (FUSED && a.h != 0) store8<D>(a.h + at + c * size, left, z);
+      const Group g = group_at<EDGE>(a.cols, c);
+      const v8f z = input8<D, FUSED, EDGE>(a, row, g, offset);
+      if (FUSED && a.h != 0) store8<D, EDGE>(a.h + at + g.c * size, g.left, z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = j < left ? z[j] - mean : 0.0f;
+        const float d = own<EDGE>(g, j) ? z[j] - mean : 0.0f;
         q[0] = __builtin_fmaf(d, d, q[0]);
       }
     }
     row_sum<kLong>(q, lds[1]);
     const float rstd = 1.0f / __builtin_sqrtf(q[0] * inverse + a.eps);
     for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) {
-      const int left = left_of<true>(a.cols, c);
+      const Group g = group_at<EDGE>(a.cols, c);
       v8f w = 1.0f, b = 0.0f;
-      if (a.weight != 0) w = load8<true>(a.weight_dtype, a.weight, c, left);
-      if (a.bias != 0) b = load8<true>(a.weight_dtype, a.bias, c, left);
-      store8<D>(a.y + at + c * size, left, fma8((z8(row, c) - mean) * rstd, w, b));
+      if (a.weight != 0) w = load8<EDGE>(a.weight_dtype, a.weight, g);
+      if (a.bias != 0) b = load8<EDGE>(a.weight_dtype, a.bias, g);
+      const v8f z = input8<D, FUSED, EDGE>(a, row, g, offset);
+      store8<D, EDGE>(a.y + at + g.c * size, g.left, fma8((z - mean) * rstd, w, b));
     }
     if (threadIdx.x == 0) put_stats(a.stats, row, mean, rstd);
   }
@@ -226,23 +230,22 @@ struct Backward {
   DropSpec drop;
 };
 
-template <int D, bool TAIL>
-__device__ __forceinline__ void store_grads(const Backward& a, uint32_t row, uint32_t c, int left, v8f d,
-                                            uint64_t offset) {
+template <int D, int EDGE>
+__device__ __forceinline__ void store_grads(const Backward& a, uint32_t row, const Group& g, v8f d, uint64_t offset) {
   constexpr uint32_t size = sizeof(typename Of<D>::one);
-  const uint64_t at = static_cast<uint64_t>(row) * a.cols * size;
-  if (a.grad_h != 0) d = d + widen<D>(load_raw<D, TAIL>(a.grad_h + row * a.grad_h_row + c * size, left));
-  store8<D, TAIL>(a.dh + at + c * size, left, d);
+  const uint64_t at = static_cast<uint64_t>(row) * a.cols * size + g.c * size;
+  if (a.grad_h != 0) d = d + widen<D>(load_raw<D, EDGE>(a.grad_h + row * a.grad_h_row + g.c * size, g.left));
+  store8<D, EDGE>(a.dh + at, g.left, d);
   if (a.drop.limit != 0) {
-    d = drop8(d, static_cast<uint64_t>(row) * a.cols + c, offset, a.drop);
-    store8<D, TAIL>(a.dx + at + c * size, left, d);
+    d = drop8(d, static_cast<uint64_t>(row) * a.cols + g.c, offset, a.drop);
+    store8<D, EDGE>(a.dx + at, g.left, d);
   }
 }
 
 // The next row is loaded while this one is worked on (8192 x 8192 in fp32: 195 us,
 // 199 without), except by 1024 lanes, whose 128 registers do not hold it, nor the
 // weights.
-template <int D, int LANES, int K, bool TAIL>
+template <int D, int LANES, int K, int EDGE>
 __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel(Backward a) {
   constexpr uint32_t size = sizeof(typename Of<D>::one);
   constexpr uint32_t THREADS = norm_back_threads(LANES), ROWS = THREADS / LANES;
@@ -252,19 +255,18 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
   const uint64_t offset = offset_of(a.drop);
   const float inverse = 1.0f / static_cast<float>(a.cols);
   v8f w[K], dw[K], db[K];
-  int left[K];
+  Group g[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const uint32_t c = (lane + k * LANES) * 8;
-    left[k] = left_of<TAIL>(a.cols, c);
+    g[k] = group_at<EDGE>(a.cols, (lane + k * LANES) * 8);
     w[k] = 1.0f;
     dw[k] = db[k] = 0.0f;
-    if (AHEAD && left[k] > 0 && a.weight != 0) w[k] = load8<TAIL>(a.weight_dtype, a.weight, c, left[k]);
+    if (AHEAD && g[k].left > 0 && a.weight != 0) w[k] = load8<EDGE>(a.weight_dtype, a.weight, g[k]);
   }
   auto weigh = [&](int k, v8f x) __attribute__((always_inline)) {
     if constexpr (AHEAD) return x * w[k];
-    if (left[k] <= 0 || a.weight == 0) return x;
-    return x * load8<TAIL>(a.weight_dtype, a.weight, (lane + k * LANES) * 8, left[k]);
+    if (g[k].left <= 0 || a.weight == 0) return x;
+    return x * load8<EDGE>(a.weight_dtype, a.weight, g[k]);
   };
   Raw<D> dy_next[K], h_next[K];
   float2 stats_next = {};
@@ -272,11 +274,10 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
     stats_next = get_stats(a.stats, r);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t c = (lane + k * LANES) * 8;
       dy_next[k] = h_next[k] = Raw<D>{};
-      if (left[k] <= 0) continue;
-      dy_next[k] = load_raw<D, TAIL>(a.dy + r * a.dy_row + c * size, left[k]);
-      h_next[k] = load_raw<D, TAIL>(a.h + r * a.h_row + c * size, left[k]);
+      if (g[k].left <= 0) continue;
+      dy_next[k] = load_raw<D, EDGE>(a.dy + r * a.dy_row + g[k].c * size, g[k].left);
+      h_next[k] = load_raw<D, EDGE>(a.h + r * a.h_row + g[k].c * size, g[k].left);
     }
   };
   uint32_t row = blockIdx.x * ROWS + mine;
@@ -294,11 +295,11 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (!AHEAD) __builtin_amdgcn_sched_barrier(0);
-      const v8f n = (widen<D>(h[k]) - mean) * rstd, d = widen<D>(dy[k]), g = weigh(k, d);
+      const v8f n = (widen<D>(h[k]) - mean) * rstd, d = widen<D>(dy[k]), x = weigh(k, d);
       dw[k] = fma8(d, n, dw[k]);
       db[k] = db[k] + d;
-      s[0] += total(g);
-      s[1] += total(g * n);
+      s[0] += total<EDGE>(x, g[k]);
+      s[1] += total<EDGE>(x * n, g[k]);
     }
     row_sum<LANES>(s, lds[turn]);
     s[0] *= inverse;
@@ -306,9 +307,8 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (!AHEAD) __builtin_amdgcn_sched_barrier(0);
-      const v8f n = (widen<D>(h[k]) - mean) * rstd, g = weigh(k, widen<D>(dy[k]));
-      if (left[k] > 0)
-        store_grads<D, TAIL>(a, row, (lane + k * LANES) * 8, left[k], (fma8(n, v8f(-s[1]), g) - s[0]) * rstd, offset);
+      const v8f n = (widen<D>(h[k]) - mean) * rstd, x = weigh(k, widen<D>(dy[k]));
+      if (g[k].left > 0) store_grads<D, EDGE>(a, row, g[k], (fma8(n, v8f(-s[1]), x) - s[0]) * rstd, offset);
     }
     if (!AHEAD && row + step < a.rows) fetch(row + step);
   }
@@ -317,30 +317,32 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
   if constexpr (ROWS == 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t c = (lane + k * LANES) * 8;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (c + j < a.cols) {
-          to[c + j] = dw[k][j];
-          to[a.cols + c + j] = db[k][j];
+        if (j < g[k].left) {
+          to[g[k].c + j] = dw[k][j];
+          to[a.cols + g[k].c + j] = db[k][j];
         }
       }
     }
   } else {
     // the rows of the workgroup side by side in LDS, a column to a thread
-    constexpr int WIDTH = LANES * K * 8;
+    constexpr uint32_t WIDTH = LANES * K * 8;
     __shared__ float part[ROWS * WIDTH];
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        *reinterpret_cast<v8f*>(part + mine * WIDTH + (lane + k * LANES) * 8) = which ? db[k] : dw[k];
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < g[k].left) part[mine * WIDTH + g[k].c + j] = which ? db[k][j] : dw[k][j];
+      }
       __syncthreads();
       for (uint32_t c = threadIdx.x; c < a.cols; c += THREADS) {
         float x = part[c];
 #pragma unroll
-        for (int r = 1; r < ROWS; ++r) x += part[r * WIDTH + c];
+        for (uint32_t r = 1; r < ROWS; ++r) x += part[r * WIDTH + c];
         to[which * a.cols + c] = x;
       }
     }
@@ -350,6 +352,7 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
 template <int D>
 __global__ __launch_bounds__(kLong) void norm_backward_long_kernel(Backward a) {
   constexpr uint32_t size = sizeof(typename Of<D>::one);
+  constexpr int EDGE = kShifted;
   __shared__ float lds[2][kLong / 64 * 2];
   const uint64_t offset = offset_of(a.drop);
   const float inverse = 1.0f / static_cast<float>(a.cols);
@@ -361,24 +364,23 @@ __global__ __launch_bounds__(kLong) void norm_backward_long_kernel(Backward a) {
     float s[2] = {0.0f, 0.0f};
     for (int pass = 0; pass < 2; ++pass) {
       for (uint32_t c = threadIdx.x * 8; c < a.cols; c += kLong * 8) {
-        const int left = left_of<true>(a.cols, c);
-        const v8f dy = load8<D>(a.dy + row * a.dy_row + c * size, left);
-        const v8f n = (load8<D>(a.h + row * a.h_row + c * size, left) - stats.x) * stats.y;
-        v8f g = dy;
-        if (a.weight != 0) g = g * load8<true>(a.weight_dtype, a.weight, c, left);
+        const Group g = group_at<EDGE>(a.cols, c);
+        const v8f dy = widen<D>(load_raw<D, EDGE>(a.dy + row * a.dy_row + g.c * size, g.left));
+        const v8f n = (widen<D>(load_raw<D, EDGE>(a.h + row * a.h_row + g.c * size, g.left)) - stats.x) * stats.y;
+        v8f x = dy;
+        if (a.weight != 0) x = x * load8<EDGE>(a.weight_dtype, a.weight, g);
         if (pass == 1) {
-          store_grads<D, true>(a, row, c, left, (fma8(n, v8f(-s[1]), g) - s[0]) * stats.y, offset);
+          store_grads<D, EDGE>(a, row, g, (fma8(n, v8f(-s[1]), x) - s[0]) * stats.y, offset);
           continue;
         }
-        s[0] += total(g);
-        s[1] += total(g * n);
+        s[0] += total<EDGE>(x, g);
+        s[1] += total<EDGE>(x * n, g);
         if (to != nullptr) {   // the workgroup's own sums, each element always by the same lane
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            if (j < left) {
-              to[c + j] = __builtin_fmaf(dy[j], n[j], first ? 0.0f : to[c + j]);
-              to[a.cols + c + j] = dy[j] + (first ? 0.0f : to[a.cols + c + j]);
-            }
+            if (!own<EDGE>(g, j)) continue;
+            to[g.c + j] = __builtin_fmaf(dy[j], n[j], first ? 0.0f : to[g.c + j]);
+            to[a.cols + g.c + j] = dy[j] + (first ? 0.0f : to[a.cols + g.c + j]);
           }
         }
       }
@@ -437,7 +439,7 @@ struct Drop {
 };
 constexpr int kDropThreads = 256;
 
-template <int D, bool FLAT, int UNROLL>
+template <int D, bool FLAT, int EDGE, int UNROLL>
 __global__ __launch_bounds__(kDropThreads) void dropout_kernel(Drop a) {
   typedef typename Of<D>::one one;
   constexpr int kTile = kDropThreads * UNROLL;
@@ -445,7 +447,8 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(Drop a) {
   for (int64_t tile = static_cast<int64_t>(blockIdx.x) * kTile; tile < a.groups;
        tile += static_cast<int64_t>(gridDim.x) * kTile) {
     int64_t row[UNROLL], c[UNROLL];
-    v8f x[UNROLL], r[UNROLL];
+    int left[UNROLL];
+    Raw<D> x[UNROLL], r[UNROLL];
     const int64_t row0 = FLAT ? 0 : tile / a.row_groups;
     const uint32_t rest = FLAT ? 0 : static_cast<uint32_t>(tile - row0 * a.row_groups);
 #pragma unroll
@@ -459,20 +462,22 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(Drop a) {
         row[u] = row0 + q;
         c[u] = static_cast<int64_t>(rest + i - q * a.row_groups) * 8;
       }
-      x[u] = r[u] = 0.0f;
-      if (tile + i < a.groups) {
-        x[u] = load8<D>(a.x + (row[u] * a.x_stride + c[u]) * sizeof(one), a.cols - c[u]);
-        if (a.residual != 0) r[u] = load8<D>(a.residual + (row[u] * a.residual_stride + c[u]) * sizeof(one), a.cols - c[u]);
+      left[u] = tile + i < a.groups ? static_cast<int>(min(a.cols - c[u], int64_t(8))) : 0;
+      if (EDGE == kShifted && left[u] > 0 && left[u] < 8) c[u] = a.cols - 8;
+      x[u] = r[u] = Raw<D>{};
+      if (left[u] > 0) {
+        x[u] = load_raw<D, EDGE>(a.x + (row[u] * a.x_stride + c[u]) * sizeof(one), left[u]);
+        if (a.residual != 0) r[u] = load_raw<D, EDGE>(a.residual + (row[u] * a.residual_stride + c[u]) * sizeof(one), left[u]);
       }
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      if (tile + u * kDropThreads + threadIdx.x >= a.groups) continue;
+      if (left[u] <= 0) continue;
       const int64_t first = row[u] * a.cols + c[u];
-      v8f z = x[u];
+      v8f z = widen<D>(x[u]);
       if (a.drop.limit != 0) z = drop8(z, static_cast<uint64_t>(first), offset, a.drop);
-      if (a.residual != 0) z = z + r[u];
-      store8<D>(a.y + first * sizeof(one), a.cols - c[u], z);
+      if (a.residual != 0) z = z + widen<D>(r[u]);
+      store8<D, EDGE>(a.y + first * sizeof(one), left[u], z);
     }
   }
 }
@@ -509,8 +514,10 @@ void launch_forward(const Forward& a, hipStream_t s) {
   };
   const bool short_row = by_shape(a.cols, [&](auto lanes, auto groups) {
     constexpr int L = decltype(lanes)::value, K = decltype(groups)::value, T = norm_threads(L);
-    if (a.cols % 8 != 0) go(norm_forward_kernel<D, L, K, FUSED, true>, T, T / L);
-    else go(norm_forward_kernel<D, L, K, FUSED, false>, T, T / L);
+    if (a.cols % 8 == 0) return go(norm_forward_kernel<D, L, K, FUSED, kWhole>, T, T / L);
+    if constexpr (L == 16)
+      if (a.cols < 8) return go(norm_forward_kernel<D, L, K, FUSED, kSmall>, T, T / L);
+    go(norm_forward_kernel<D, L, K, FUSED, kShifted>, T, T / L);
   });
   if (!short_row) go(norm_forward_long_kernel<D, FUSED>, kLong, 1);
 }
@@ -520,8 +527,10 @@ void launch_backward(const Backward& a, unsigned blocks, hipStream_t s) {
   auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(threads), 0, s, a); };
   const bool short_row = by_shape(a.cols, [&](auto lanes, auto groups) {
     constexpr int L = decltype(lanes)::value, K = decltype(groups)::value, T = norm_back_threads(L);
-    if (a.cols % 8 != 0) go(norm_backward_kernel<D, L, K, true>, T);
-    else go(norm_backward_kernel<D, L, K, false>, T);
+    if (a.cols % 8 == 0) return go(norm_backward_kernel<D, L, K, kWhole>, T);
+    if constexpr (L == 16)
+      if (a.cols < 8) return go(norm_backward_kernel<D, L, K, kSmall>, T);
+    go(norm_backward_kernel<D, L, K, kShifted>, T);
   });
   if (!short_row) go(norm_backward_long_kernel<D>, kLong);
 }
@@ -587,10 +596,19 @@ class HipLayersDevice final : public LayersDevice {
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(grid_of((d.groups + tile - 1) / tile, 1 << 20)), dim3(kDropThreads), 0, s, d);
     };
+    // Groups that are written twice must not be read after the first time: in
+    // place (and in a flat array, of which it is one group) the last one is cut.
+    const bool whole = d.cols % 8 == 0, cut = d.cols < 8 || a.y == a.x.data || a.y == a.residual.data;
     by_type(a.dtype, [&](auto t) {
       constexpr int D = decltype(t)::value;
-      if (flat) many ? go(dropout_kernel<D, true, 4>) : go(dropout_kernel<D, true, 1>);
-      else many ? go(dropout_kernel<D, false, 4>) : go(dropout_kernel<D, false, 1>);
+      auto pick = [&](auto unroll) {
+        constexpr int U = decltype(unroll)::value;
+        if (flat) whole ? go(dropout_kernel<D, true, kWhole, U>) : go(dropout_kernel<D, true, kSmall, U>);
+        else if (whole) go(dropout_kernel<D, false, kWhole, U>);
+        else cut ? go(dropout_kernel<D, false, kSmall, U>) : go(dropout_kernel<D, false, kShifted, U>);
+      };
+      if (many) pick(std::integral_constant<int, 4>());
+      else pick(std::integral_constant<int, 1>());
     });
     HIP_OK(hipGetLastError(), "launch dropout_kernel");
     return kOk;

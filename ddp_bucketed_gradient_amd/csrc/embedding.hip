@@ -5,14 +5,13 @@
 namespace ddpb {
 namespace {
 
-// A token of 4 or 8 bytes; what lies outside of the table becomes `vocab`.
-__device__ __forceinline__ uint32_t token_at(uint64_t tokens, int32_t bytes, int64_t i, uint32_t vocab) {
-  if (bytes == 4) {
-    const uint32_t t = G<const uint32_t>(tokens)[i];
-    return t < vocab ? t : vocab;
-  }
-  const uint64_t t = G<const uint64_t>(tokens)[i];
-  return t < vocab ? static_cast<uint32_t>(t) : vocab;
+// A token of 4 or 8 bytes; what lies outside of the table becomes `vocab`. Without
+// a branch, so that several can be loaded together: the upper half of a token of
+// four bytes is read where the lower one is, and left out.
+__device__ __forceinline__ uint32_t token_at(uint64_t tokens, uint32_t bytes, uint32_t i, uint32_t vocab) {
+  const uint64_t at = tokens + static_cast<uint64_t>(i) * bytes;
+  const uint32_t low = *G<const uint32_t>(at), high = *G<const uint32_t>(at + (bytes - 4));
+  return (bytes == 4 || high == 0) && low < vocab ? low : vocab;
 }
 
 // ---------------------------------------------------------------------------
@@ -21,7 +20,7 @@ struct Lookup {
   uint64_t tokens, table, residual, y;
   uint64_t residual_row;        // bytes from row to row
   uint32_t n, cols, vocab, slice, shift;
-  int32_t token_bytes;
+  uint32_t token_bytes;
   float scale;
 };
 
@@ -43,7 +42,7 @@ __global__ __launch_bounds__(256) void lookup_kernel(Lookup a) {
     Raw<D> r[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
-      t[k] = first + k < a.n ? token_at(a.tokens, a.token_bytes, first + k, a.vocab) : a.vocab;
+      t[k] = token_at(a.tokens, a.token_bytes, min(first + k, a.n - 1), a.vocab);
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       x[k] = Raw<TD>{};
@@ -113,26 +112,21 @@ struct Sort {
   uint32_t* joins;              // the count of the long runs, which the first launch clears
   int64_t n;
   uint32_t vocab, tiles;
-  int32_t token_bytes, shift, digit, scanned;
+  uint32_t token_bytes;
+  int32_t shift, digit, scanned;
   int32_t passes;               // of a sort by one workgroup
   Zeros zeros;
 };
 
 __device__ __forceinline__ void load_keys(const Sort& a, int64_t tile, uint32_t (&key)[kSortKeys], uint32_t (&place)[kSortKeys]) {
   // a wave's keys are consecutive: 64 at a time
-  const int64_t at = tile * kSortTile + (threadIdx.x >> 6) * (64 * kSortKeys) + (threadIdx.x & 63);
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  const uint32_t at = static_cast<uint32_t>(tile * kSortTile) + (threadIdx.x >> 6) * (64 * kSortKeys) + (threadIdx.x & 63);
 #pragma unroll
   for (int e = 0; e < kSortKeys; ++e) {
-    const int64_t i = at + e * 64;
-    key[e] = place[e] = 0;
-    if (i >= a.n) continue;
-    if (a.tokens != 0) {
-      key[e] = token_at(a.tokens, a.token_bytes, i, a.vocab);
-      place[e] = static_cast<uint32_t>(i);
-    } else {
-      key[e] = a.keys_in[i];
-      place[e] = a.order_in[i];
-    }
+    const uint32_t i = min(at + e * 64, n - 1);            // (what is behind the end is not used)
+    key[e] = a.tokens != 0 ? token_at(a.tokens, a.token_bytes, i, a.vocab) : a.keys_in[i];
+    place[e] = a.tokens != 0 ? i : a.order_in[i];
   }
 }
 
@@ -231,8 +225,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_ranges_kernel(Sort a) {
   if (range == 0 && threadIdx.x == 0) *a.joins = 0;
   // a wave's share of the tokens is consecutive
   const uint32_t each = (n + kSortThreads - 1) / kSortThreads * 64, from = wave * each, to = min(from + each, n);
-#pragma unroll 4
-  for (uint32_t i = from + lane; i < to; i += 64) s.token[i] = token_at(a.tokens, a.token_bytes, i, a.vocab);
+  for (uint32_t i = from + lane; i < to; i += 64 * 4) {
+    uint32_t t[4];
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e) t[e] = token_at(a.tokens, a.token_bytes, min(i + e * 64, to - 1), a.vocab);
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e)
+      if (i + e * 64 < to) s.token[i + e * 64] = t[e];
+  }
   uint32_t mine = 0, below = 0;
   for (uint32_t i = from; i < to; i += 64) {
     const uint32_t t = i + lane < to ? s.token[i + lane] : a.vocab;
@@ -602,7 +602,7 @@ int enqueue_lookup(const LookupArgs& a, std::string* err) {
   const Lookup l = {addr(a.tokens), addr(a.table), addr(a.residual.data), addr(a.y),
                     static_cast<uint64_t>(a.residual.stride * dtype_size(a.dtype)), static_cast<uint32_t>(a.n),
                     static_cast<uint32_t>(a.cols), static_cast<uint32_t>(a.vocab),
-                    static_cast<uint32_t>((groups + slices - 1) / slices), shift, a.token_bytes, a.scale};
+                    static_cast<uint32_t>((groups + slices - 1) / slices), shift, static_cast<uint32_t>(a.token_bytes), a.scale};
   hipStream_t s = static_cast<hipStream_t>(a.stream);
   const int64_t rows = (256 >> shift) * kRows, want = (a.n + rows - 1) / rows;         // rows of a workgroup
   const dim3 grid(static_cast<unsigned>(want < (1 << 20) ? want : 1 << 20), static_cast<unsigned>(slices));
@@ -629,7 +629,7 @@ int enqueue_lookup_backward(const LookupBackwardArgs& a, std::string* err) {
   k.n = a.n;
   k.vocab = static_cast<uint32_t>(a.vocab);
   k.tiles = static_cast<uint32_t>(p.tiles);
-  k.token_bytes = a.token_bytes;
+  k.token_bytes = static_cast<uint32_t>(a.token_bytes);
   k.digit = p.digit;
   k.passes = p.passes;
   k.hist = words(p.hist);

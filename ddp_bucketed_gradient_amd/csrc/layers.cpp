@@ -9,8 +9,7 @@ namespace ddpb {
 namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
-constexpr int64_t kMaxNormCols = int64_t(1) << 20;
-constexpr int64_t kMaxLookupCols = int64_t(1) << 24;
+constexpr int64_t kMaxCols = int64_t(1) << 20;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSplitCols = int64_t(1) << 33;   // their groups are counted in 32 bits
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
@@ -92,7 +91,7 @@ int32_t norm_backward_blocks(int64_t rows, int64_t cols) {
 }
 
 bool norm_sizes_ok(int64_t rows, int64_t cols) {
-  return rows >= 0 && rows <= kMaxRows && cols >= 1 && cols <= kMaxNormCols && (rows == 0 || cols <= kMaxElems / rows);
+  return rows >= 0 && rows <= kMaxRows && cols >= 1 && cols <= kMaxCols && (rows == 0 || cols <= kMaxElems / rows);
 }
 
 int64_t norm_backward_workspace(int64_t rows, int64_t cols) {
@@ -173,7 +172,7 @@ int check(const DropoutArgs& a, std::string* err) {
 }
 
 bool lookup_sizes_ok(int64_t n, int64_t vocab, int64_t cols) {
-  return n >= 0 && n <= kMaxTokens && vocab >= 0 && vocab <= kMaxRows - 1 && cols >= 1 && cols <= kMaxLookupCols &&
+  return n >= 0 && n <= kMaxTokens && vocab >= 0 && vocab <= kMaxRows - 1 && cols >= 1 && cols <= kMaxCols &&
          (n == 0 || cols <= kMaxElems / n) && (vocab == 0 || cols <= kMaxElems / vocab);
 }
 
@@ -181,7 +180,7 @@ int check(const LookupArgs& a, std::string* err) {
   const char* what = "embedding";
   const int64_t size = dtype_size(a.dtype), ts = dtype_size(a.table_dtype);
   if (!lookup_sizes_ok(a.n, a.vocab, a.cols))
-    return fail(err, what, "tokens must be 0..2^30, the table 0..2^31 - 2 rows of 1..2^24");
+    return fail(err, what, "tokens must be 0..2^30, the table 0..2^31 - 2 rows of 1..2^20");
   if (!std::isfinite(a.scale)) return fail(err, what, "scale must be finite in fp32");
   if (!array_ok(a.tokens, a.n, a.token_bytes) || !array_ok(a.table, a.vocab, ts) ||
       !matrix_ok(a.residual, a.n, size, false))
@@ -236,7 +235,7 @@ int check(const LookupBackwardArgs& a, std::string* err) {
   const char* what = "embedding_backward";
   const int64_t size = dtype_size(a.dtype), gs = dtype_size(a.grad_dtype);
   if (!lookup_sizes_ok(a.n, a.vocab, a.cols))
-    return fail(err, what, "tokens must be 0..2^30, the table 0..2^31 - 2 rows of 1..2^24");
+    return fail(err, what, "tokens must be 0..2^30, the table 0..2^31 - 2 rows of 1..2^20");
   if (!std::isfinite(a.scale)) return fail(err, what, "scale must be finite in fp32");
   if (!array_ok(a.tokens, a.n, a.token_bytes) || !matrix_ok(a.dy, a.n, size, true))
     return fail(err, what, "NULL, misaligned or too widely spread input");

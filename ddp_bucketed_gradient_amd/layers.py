@@ -188,6 +188,38 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, drop
     return Normed(y, h, stats)
 
 
+def _norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulate, lib):
+    """layer_norm_backward in two steps: the checks, and what they return, the call."""
+    torch = _t()
+    code, dev = _code(dy.dtype, "dy"), dy.device
+    rows, cols, stride = _rows(dy, "dy")
+    hs = _rows(h, "h", dy)[2]
+    gs = 0 if grad_h is None else _rows(grad_h, "grad_h", dy)[2]
+    st = _vector(stats, "stats", 2 * rows, dev, torch.float32)
+    w = _vector(weight, "weight", cols, dev)
+    wc = code if weight is None else _code(weight.dtype, "weight")
+    gt = dweight.dtype if dweight is not None else dbias.dtype if dbias is not None else torch.float32
+    dw, db = _vector(dweight, "dweight", cols, dev, gt), _vector(dbias, "dbias", cols, dev, gt)
+    gc = _code(gt, "dweight and dbias")
+    dropped = drop is not None and drop.active
+    spec = drop._on(dev) if dropped else None
+    lib = _lib(lib)
+
+    def run():
+        ws = None
+        if dw or db:
+            ws = torch.empty(lib.layer_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
+        dh = _like(dy)
+        dx = _like(dy) if dropped else dh
+        _call(dev, lib.layer_norm_backward, rows, cols, code, dy.data_ptr(), stride, h.data_ptr(), hs, st,
+              0 if grad_h is None else grad_h.data_ptr(), gs, spec, w, wc, dh.data_ptr(),
+              dx.data_ptr() if dropped else 0, dw, db, gc, accumulate, 0 if ws is None else ws.data_ptr(),
+              0 if ws is None else ws.numel())
+        _wrote(dweight, dbias)
+        return NormGrads(dx, dh)
+    return run
+
+
 def layer_norm_backward(dy, h, stats, weight=None, dweight=None, dbias=None, grad_h=None,
                         drop: Optional[Drop] = None, accumulate: bool = False,
                         lib: Optional[_abi.Lib] = None) -> NormGrads:
@@ -196,29 +228,7 @@ def layer_norm_backward(dy, h, stats, weight=None, dweight=None, dbias=None, gra
     wanted; one type): written, or with ``accumulate`` added to. ``grad_h``: a
     gradient that reaches h from elsewhere, as where h itself goes on as the
     next residual."""
-    torch = _t()
-    code, dev = _code(dy.dtype, "dy"), dy.device
-    rows, cols, stride = _rows(dy, "dy")
-    hs = _rows(h, "h", dy)[2]
-    gs = 0 if grad_h is None else _rows(grad_h, "grad_h", dy)[2]
-    st = _vector(stats, "stats", 2 * rows, dev, torch.float32)
-    w = _vector(weight, "weight", cols, dev)
-    gt = dweight.dtype if dweight is not None else dbias.dtype if dbias is not None else torch.float32
-    dw, db = _vector(dweight, "dweight", cols, dev, gt), _vector(dbias, "dbias", cols, dev, gt)
-    lib = _lib(lib)
-    ws = None
-    if dw or db:
-        ws = torch.empty(lib.layer_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
-    dh = _like(dy)
-    dropped = drop is not None and drop.active
-    dx = _like(dy) if dropped else dh
-    _call(dev, lib.layer_norm_backward, rows, cols, code, dy.data_ptr(), stride, h.data_ptr(), hs, st,
-          0 if grad_h is None else grad_h.data_ptr(), gs, drop._on(dev) if dropped else None, w,
-          code if weight is None else _code(weight.dtype, "weight"), dh.data_ptr(), dx.data_ptr() if dropped else 0,
-          dw, db, _code(gt, "dweight and dbias"), accumulate, 0 if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel())
-    _wrote(dweight, dbias)
-    return NormGrads(dx, dh)
+    return _norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulate, lib)()
 
 
 def _tokens(tokens, device):
@@ -251,12 +261,8 @@ def embedding(tokens, table, scale: float = 1.0, residual=None, dtype=None, lib:
     return y
 
 
-def embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bool = False,
-                       lib: Optional[_abi.Lib] = None):
-    """The gradient of embedding's table (the residual's is dy): row v of
-    ``dtable`` becomes ``scale`` times the sum of dy over the places of token v,
-    in their order; with ``accumulate`` that is added to it. Tokens outside of the
-    table are left out. Returns dtable."""
+def _embedding_backward(dy, tokens, dtable, scale, accumulate, lib):
+    """embedding_backward in two steps: the checks, and what they return, the call."""
     torch = _t()
     vocab, cols, gc = _table(dtable, "dtable")
     dev = dtable.device
@@ -266,8 +272,20 @@ def embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bool 
     stride = _rows(dy, "dy")[2]
     code = _code(dy.dtype, "dy")
     lib = _lib(lib)
-    ws = torch.empty(lib.embedding_backward_workspace_bytes(n, vocab, cols), dtype=torch.uint8, device=dev)
-    _call(dev, lib.embedding_backward, n, at, size, vocab, cols, dy.data_ptr(), stride, code, scale,
-          dtable.data_ptr(), gc, accumulate, ws.data_ptr(), ws.numel())
-    _wrote(dtable)
-    return dtable
+
+    def run():
+        ws = torch.empty(lib.embedding_backward_workspace_bytes(n, vocab, cols), dtype=torch.uint8, device=dev)
+        _call(dev, lib.embedding_backward, n, at, size, vocab, cols, dy.data_ptr(), stride, code, scale,
+              dtable.data_ptr(), gc, accumulate, ws.data_ptr(), ws.numel())
+        _wrote(dtable)
+        return dtable
+    return run
+
+
+def embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bool = False,
+                       lib: Optional[_abi.Lib] = None):
+    """The gradient of embedding's table (the residual's is dy): row v of
+    ``dtable`` becomes ``scale`` times the sum of dy over the places of token v,
+    in their order; with ``accumulate`` that is added to it. Tokens outside of the
+    table are left out. Returns dtable."""
+    return _embedding_backward(dy, tokens, dtable, scale, accumulate, lib)()

@@ -288,8 +288,9 @@ class Reducer:
             raise ValueError("weight and bias are two variables")
         self._writable(vs, dy, h, stats, weight, grad_h, drop)
         to = lambda r, v: None if v is None else self._grads[r][v]  # noqa: E731
-        out = [_layers.layer_norm_backward(dy[r], h[r], stats[r], weight[r], to(r, weight_var), to(r, bias_var),
-                                           grad_h[r], drop[r], accumulate, lib=self.lib) for r in range(self.R)]
+        calls = [_layers._norm_backward(dy[r], h[r], stats[r], weight[r], to(r, weight_var), to(r, bias_var),
+                                        grad_h[r], drop[r], accumulate, self.lib) for r in range(self.R)]
+        out = [run() for run in calls]
         self.lib.mark_ready_many(self.h, vs)
         return out
 
@@ -300,9 +301,9 @@ class Reducer:
         self._writable([v], dy, tokens)
         if len(self.shapes[v]) != 2:
             raise ValueError(f"variable {v} has shape {self.shapes[v]}, not two dimensions")
-        for r in range(self.R):
-            _layers.embedding_backward(dy[r], tokens[r], self._grads[r][v].view(self.shapes[v]), scale, accumulate,
-                                       lib=self.lib)
+        for run in [_layers._embedding_backward(dy[r], tokens[r], self._grads[r][v].view(self.shapes[v]), scale,
+                                                accumulate, self.lib) for r in range(self.R)]:
+            run()
         self.lib.mark_ready(self.h, v)
 
     # -- after the synchronisation -------------------------------------------------------

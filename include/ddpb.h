@@ -596,7 +596,7 @@ int ddpb_layer_norm_backward(int64_t rows, int64_t cols, int32_t dtype, const vo
 /* y_i = scale * table[tokens[i]] + residual_i for n tokens of 4 or 8 bytes
  * (int32_t, int64_t); residual may be NULL. A token outside of 0 .. vocab - 1
  * stands for a row of zeros and takes no gradient (padding; the other parts of a
- * table that is split by rows). n <= 2^30, vocab <= 2^31 - 2, 1 <= cols <= 2^24. */
+ * table that is split by rows). n <= 2^30, vocab <= 2^31 - 2, 1 <= cols <= 2^20. */
 int ddpb_embedding(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols, const void* table,
                    int32_t table_dtype, double scale, const void* residual, int64_t residual_stride, void* y,
                    int32_t dtype, void* stream);

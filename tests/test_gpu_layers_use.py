@@ -214,6 +214,10 @@ def test_reducer_refuses_before_it_writes():
     with torch.cuda.stream(torch.cuda.Stream()):
         with pytest.raises(ValueError, match="compute stream"):
             red.embedding_backward(0, d, toks)
+    with pytest.raises(ValueError):                   # the second replica's: nothing is written for the first
+        red.embedding_backward(0, [d[0], d[1][:2]], toks)
+    with pytest.raises(ValueError):
+        red.layer_norm_backward(4, 5, d, [d[0], d[1][:2]], st)
     assert all((g == 9).all() for row in grads for g in row)
     red.embedding_backward(0, d, toks)
     before = grads[0][0].clone()

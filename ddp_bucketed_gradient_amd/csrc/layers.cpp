@@ -81,13 +81,24 @@ NormShape norm_shape(int64_t cols) {
   return {0, 0};
 }
 
-int32_t norm_backward_blocks(int64_t rows, int64_t cols) {
+namespace {
+// Rows that a workgroup of the backward pass takes at once.
+int64_t rows_at_once(NormShape s) { return s.lanes == 0 || s.lanes > 64 ? 1 : 512 / s.lanes; }
+}  // namespace
+
+bool norm_backward_alone(int64_t rows, int64_t cols) {
   const NormShape s = norm_shape(cols);
-  // rows of a workgroup at once, and workgroups that leave a partial sum: eight waves a CU
-  const int64_t at_once = s.lanes == 0 || s.lanes > 64 ? 1 : 512 / s.lanes;
+  return s.lanes != 0 && rows > 0 && rows <= 4 * rows_at_once(s);
+}
+
+int32_t norm_backward_blocks(int64_t rows, int64_t cols) {
+  if (norm_backward_alone(rows, cols)) return 1;
+  const NormShape s = norm_shape(cols);
+  // workgroups that leave a partial sum: eight waves a CU
   int64_t most = s.lanes == 256 ? 512 : 256;
   if (s.lanes == 0) most = std::max<int64_t>(32, std::min<int64_t>(256, (int64_t(64) << 20) / (8 * cols)));
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min(most, (rows + at_once - 1) / at_once)));
+  const int64_t need = (rows + rows_at_once(s) - 1) / rows_at_once(s);
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min(most, need)));
 }
 
 bool norm_sizes_ok(int64_t rows, int64_t cols) {
@@ -95,6 +106,7 @@ bool norm_sizes_ok(int64_t rows, int64_t cols) {
 }
 
 int64_t norm_backward_workspace(int64_t rows, int64_t cols) {
+  if (rows == 0 || norm_backward_alone(rows, cols)) return 0;
   return up256(static_cast<int64_t>(norm_backward_blocks(rows, cols)) * 2 * cols * 4);
 }
 

@@ -225,10 +225,23 @@ struct Backward {
   uint64_t dy, h, stats, grad_h, weight, dh, dx;
   uint64_t dy_row, h_row, grad_h_row;           // bytes from row to row
   float* partials;                              // [workgroup][dweight, dbias][cols], or NULL
+  uint64_t dweight, dbias;                      // one workgroup: written by it (else 0)
   uint32_t rows, cols;
-  int32_t weight_dtype;
+  int32_t weight_dtype, grad_dtype, accumulate;
   DropSpec drop;
 };
+
+// Writes, or adds to, one element of a gradient.
+__device__ __forceinline__ void put_grad(uint64_t to, int dtype, bool add, uint32_t c, float x) {
+  auto put = [&](auto one) {
+    auto* p = G<decltype(one)>(to + c * static_cast<uint32_t>(sizeof(one)));
+    if (add) x += static_cast<float>(*p);
+    *p = static_cast<decltype(one)>(x);
+  };
+  if (dtype == kF32) put(float());
+  else if (dtype == kBF16) put(__bf16());
+  else put(_Float16());
+}
 
 template <int D, int EDGE>
 __device__ __forceinline__ void store_grads(const Backward& a, uint32_t row, const Group& g, v8f d, uint64_t offset) {
@@ -312,16 +325,22 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
     }
     if (!AHEAD && row + step < a.rows) fetch(row + step);
   }
-  if (a.partials == nullptr) return;
+  const bool alone = (a.dweight | a.dbias) != 0;
+  if (a.partials == nullptr && !alone) return;
   float* to = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+  auto put = [&](int which, uint32_t c, float x) __attribute__((always_inline)) {
+    const uint64_t grad = which ? a.dbias : a.dweight;
+    if (!alone) to[which * a.cols + c] = x;
+    else if (grad != 0) put_grad(grad, a.grad_dtype, a.accumulate != 0, c, x);
+  };
   if constexpr (ROWS == 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (j < g[k].left) {
-          to[g[k].c + j] = dw[k][j];
-          to[a.cols + g[k].c + j] = db[k][j];
+        if (g[k].left > 0 && own<EDGE>(g[k], j)) {
+          put(0, g[k].c + j, dw[k][j]);
+          put(1, g[k].c + j, db[k][j]);
         }
       }
     }
@@ -343,7 +362,7 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
         float x = part[c];
 #pragma unroll
         for (uint32_t r = 1; r < ROWS; ++r) x += part[r * WIDTH + c];
-        to[which * a.cols + c] = x;
+        put(which, c, x);
       }
     }
   }
@@ -415,15 +434,7 @@ __global__ __launch_bounds__(kWeightCols * kWeightWaves) void norm_weights_kerne
   if (wave != 0 || c >= cols) return;
 #pragma unroll
   for (int w = 1; w < kWeightWaves; ++w) x += part[w][threadIdx.x];
-  const uint64_t at = out + static_cast<uint64_t>(c) * (dtype == kF32 ? 4 : 2);
-  auto put = [&](auto one) {
-    auto* p = G<decltype(one)>(at);
-    if (accumulate) x += static_cast<float>(*p);
-    *p = static_cast<decltype(one)>(x);
-  };
-  if (dtype == kF32) put(float());
-  else if (dtype == kBF16) put(__bf16());
-  else put(_Float16());
+  put_grad(out, dtype, accumulate != 0, c, x);
 }
 
 // ---------------------------------------------------------------------------
@@ -562,16 +573,18 @@ class HipLayersDevice final : public LayersDevice {
     const bool weights = a.dweight != nullptr || a.dbias != nullptr;
     hipStream_t s = static_cast<hipStream_t>(a.stream);
     const int32_t blocks = norm_backward_blocks(a.rows, a.cols);
+    const bool alone = norm_backward_alone(a.rows, a.cols);
     if (a.rows > 0) {
       const Backward b = {addr(a.dy.data), addr(a.h.data), addr(a.stats), addr(a.grad_h.data), addr(a.weight),
                           addr(a.dh), addr(a.dx), bytes(a.dy.stride, a.dtype), bytes(a.h.stride, a.dtype),
                           bytes(a.grad_h.stride, a.dtype),
-                          weights ? static_cast<float*>(a.workspace) : nullptr, static_cast<uint32_t>(a.rows),
-                          static_cast<uint32_t>(a.cols), a.weight_dtype, a.drop};
+                          weights && !alone ? static_cast<float*>(a.workspace) : nullptr,
+                          alone ? addr(a.dweight) : 0, alone ? addr(a.dbias) : 0, static_cast<uint32_t>(a.rows),
+                          static_cast<uint32_t>(a.cols), a.weight_dtype, a.grad_dtype, a.accumulate ? 1 : 0, a.drop};
       by_type(a.dtype, [&](auto d) { launch_backward<decltype(d)::value>(b, static_cast<unsigned>(blocks), s); });
       HIP_OK(hipGetLastError(), "launch norm_backward_kernel");
     }
-    if (weights) {
+    if (weights && !alone) {
       hipLaunchKernelGGL(norm_weights_kernel, dim3((a.cols + kWeightCols - 1) / kWeightCols, 2),
                          dim3(kWeightCols * kWeightWaves), 0, s, static_cast<const float*>(a.workspace),
                          a.rows > 0 ? blocks : 0, static_cast<uint32_t>(a.cols), addr(a.dweight), addr(a.dbias),

@@ -109,10 +109,13 @@ NormShape norm_shape(int64_t cols);
 // weights' gradients: a function of the sizes only, so that the order of the
 // sums does not depend on the device.
 int32_t norm_backward_blocks(int64_t rows, int64_t cols);
+// Few rows: one workgroup takes them and writes the gradients itself, without a
+// workspace and a second launch (whose host time is more than its rows take).
+bool norm_backward_alone(int64_t rows, int64_t cols);
 
 // How the embedding's gradient is cut.
 constexpr int kSortThreads = 1024;
-constexpr int kSortKeys = 4;                                  // keys of a thread
+constexpr int kSortKeys = 2;                                  // keys of a thread (131072 tokens, a pass: 12.2 us, 14.8 with 4)
 constexpr int64_t kSortTile = kSortThreads * kSortKeys;       // keys of a workgroup
 constexpr int64_t kRangeKeys = 16384;                         // most tokens of a sort in one launch
 constexpr int kRanges = 32;                                   // workgroups of it

@@ -206,15 +206,14 @@ def _norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulat
     lib = _lib(lib)
 
     def run():
-        ws = None
-        if dw or db:
-            ws = torch.empty(lib.layer_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
+        nbytes = lib.layer_norm_backward_workspace_bytes(rows, cols) if dw or db else 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         dh = _like(dy)
         dx = _like(dy) if dropped else dh
         _call(dev, lib.layer_norm_backward, rows, cols, code, dy.data_ptr(), stride, h.data_ptr(), hs, st,
               0 if grad_h is None else grad_h.data_ptr(), gs, spec, w, wc, dh.data_ptr(),
               dx.data_ptr() if dropped else 0, dw, db, gc, accumulate, 0 if ws is None else ws.data_ptr(),
-              0 if ws is None else ws.numel())
+              nbytes)
         _wrote(dweight, dbias)
         return NormGrads(dx, dh)
     return run

@@ -585,7 +585,7 @@ int ddpb_layer_norm(int64_t rows, int64_t cols, int32_t dtype, const void* x, in
  * grad_h (may be NULL): a gradient that reaches h from elsewhere. dx is given if
  * drop has p > 0 (2^-17 or more), else NULL: dh is x's gradient too. dweight, dbias: NULL if not
  * wanted; with `accumulate` they are added to. The workspace is needed for those
- * two only (256-byte aligned). */
+ * two only (256-byte aligned; 0 bytes, and NULL, with few rows). */
 int ddpb_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int64_t* bytes);
 int ddpb_layer_norm_backward(int64_t rows, int64_t cols, int32_t dtype, const void* dy, int64_t dy_stride,
                              const void* h, int64_t h_stride, const float* stats, const void* grad_h,

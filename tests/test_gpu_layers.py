@@ -123,12 +123,20 @@ def test_norm_gradient_many_rows(rows):
     back_case(rows, rows, 2050, "f16", None, "f32", False, None, False, 0)
 
 
-def test_norm_gradient_parts_that_are_not_wanted():
+@pytest.mark.parametrize("rows, cols", [(128, 100), (129, 100), (4, 128), (32, 1000), (33, 1000), (4, 2001), (5, 2001),
+                                        (4, 8003), (1, 16384), (5, 16384)])
+def test_norm_gradient_by_one_workgroup_and_by_more(rows, cols):
+    back_case(rows, rows, cols, "f32", "f32", "f32", False, None, False, 0)
+    back_case(rows, rows, cols, "bf16", "f32", "bf16", True, 0.1, True, 3)
+
+
+@pytest.mark.parametrize("rows, cols", [(40, 100), (400, 100), (3, 5000)])
+def test_norm_gradient_parts_that_are_not_wanted(rows, cols):
     g = np.random.default_rng(0)
-    h, _ = make(g, (40, 100), "f32")
-    dy, _ = make(g, (40, 100), "f32")
+    h, _ = make(g, (rows, cols), "f32")
+    dy, _ = make(g, (rows, cols), "f32")
     n = D.layer_norm(h)
-    dw, db = torch.empty(100, device="cuda"), torch.empty(100, device="cuda")
+    dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
     full = D.layer_norm_backward(dy, h, n.stats, None, dw, db)
     for a, b in ((torch.empty_like(dw), None), (None, torch.empty_like(db)), (None, None)):
         out = D.layer_norm_backward(dy, h, n.stats, None, a, b)

@@ -27,7 +27,7 @@ def drop(p=0.1, at=0):
 
 NORM = dict(rows=4, cols=8, dtype=D.F32, x=A[0], x_stride=8, residual=0, residual_stride=0, drop=None, weight=A[1],
             bias=A[2], weight_dtype=D.F32, eps=1e-5, y=A[3], h=0, stats=A[4], stream=0)
-NORM_B = dict(rows=4, cols=8, dtype=D.F32, dy=A[0], dy_stride=8, h=A[1], h_stride=8, stats=A[2], grad_h=0,
+NORM_B = dict(rows=400, cols=8, dtype=D.F32, dy=A[0], dy_stride=8, h=A[1], h_stride=8, stats=A[2], grad_h=0,
               grad_h_stride=0, drop=None, weight=A[3], weight_dtype=D.F32, dh=A[4], dx=0, dweight=A[5], dbias=A[6],
               grad_dtype=D.F32, accumulate=False, workspace=A[7], ws_bytes=1 << 30, stream=0)
 DROP = dict(rows=4, cols=8, dtype=D.F32, x=A[0], x_stride=8, residual=0, residual_stride=0, drop=drop(), y=A[1], stream=0)
@@ -52,6 +52,7 @@ CALLS = {"layer_norm": NORM, "layer_norm_backward": NORM_B, "dropout": DROP, "em
     ("layer_norm", {"residual": A[0], "residual_stride": 8}),                # inputs may coincide
     ("layer_norm_backward", {"dweight": 0, "dbias": 0, "workspace": 0, "ws_bytes": 0}),
     ("layer_norm_backward", {"drop": drop(), "dx": A[7] + (1 << 38)}),
+    ("layer_norm_backward", {"rows": 100, "workspace": 0, "ws_bytes": 0}),
     ("layer_norm_backward", {"rows": 0, "dy": 0, "h": 0, "stats": 0, "dh": 0}),
     ("dropout", {"y": A[0]}),                                                # in place
     ("dropout", {"residual": A[1], "residual_stride": 8}),                   # onto the residual
@@ -146,9 +147,11 @@ def test_workspace_sizes_refused(lib, f, args):
 
 
 def test_workspaces_stay_in_bounds(lib):
-    for rows, cols in [(0, 1), (1, 1), (16384, 1024), ((1 << 31) - 1, 1), (5, 1 << 20)]:
+    for rows, cols in [(16384, 1024), ((1 << 31) - 1, 1), (5, 1 << 20), (33, 1024), (129, 128), (5, 2048)]:
         b = lib.layer_norm_backward_workspace_bytes(rows, cols)
         assert 2 * cols * 4 <= b <= 1 << 28 and b % 256 == 0
+    for rows, cols in [(0, 1), (0, 1 << 20), (1, 1), (32, 1024), (128, 128), (4, 16384)]:     # one workgroup
+        assert lib.layer_norm_backward_workspace_bytes(rows, cols) == 0
     for n, vocab, cols in [(0, 0, 1), (1, 1, 1), (16384, 30522, 1024), (1 << 30, (1 << 31) - 2, 1), (1 << 16, 5, 1 << 20)]:
         b = lib.embedding_backward_workspace_bytes(n, vocab, cols)
         # keys and order twice; histograms of at most 1024 counters for 4096 keys; two partial sums for each unit of

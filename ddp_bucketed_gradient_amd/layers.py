@@ -95,6 +95,8 @@ def _rows(t, what: str, like=None):
     cols, n = t.shape[-1], t.numel()
     if t.is_contiguous():
         return (n // cols if cols else _math.prod(t.shape[:-1])), cols, cols
+    if t.dim() == 2 and (cols == 1 or t.stride(1) == 1):
+        return n // cols, cols, t.stride(0)
     if cols != 1 and t.stride(-1) != 1:
         raise ValueError(f"the elements of a row of {what} must be consecutive")
     stride = size = None

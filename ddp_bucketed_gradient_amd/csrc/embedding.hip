@@ -415,8 +415,10 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t x, int i) {
 // BERT-large's 16384 places in bf16 into fp32: 14.4 us behind the zeros (3.4 TB/s of
 // rows in and out; four waves a CU, of which each goes through the latencies of
 // keys, rows and stores once). 131072 places of 768 columns, 40 % of them one
-// token, added to: 77 us, where the rows alone take 41 (4.4 TB/s): what a wave
-// stores stands in order before the rows it loads next.
+// token, added to: 77 us, 3.6 TB/s of scattered rows in and out (the rows of dy
+// alone: 41 us, 4.4 TB/s). Twice or four times the waves took 69-78 us (and the
+// join twice as long), finished rows collected in LDS and written eight at a
+// time 84, old rows loaded only when a run ends 89.
 template <int D, int GD, bool ADD, int EDGE>
 __global__ __launch_bounds__(256) void sum_kernel(Sum a) {
   typedef typename Of<D>::one one;

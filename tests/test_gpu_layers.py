@@ -187,6 +187,28 @@ def test_dropout_hides_what_it_drops():
     assert (D.dropout(x, D.Drop(1.0, 9, 4)) == 0).all()
 
 
+@pytest.mark.parametrize("rows, cols, pad", [(1, 1000, 0), (37, 19, 0), (37, 19, 4), (300, 7, 1), (50, 771, 2), (9, 64, 8), (2049, 13, 3)])
+def test_dropout_in_place(rows, cols, pad):
+    """Through the C call, which allows y to be x or the residual."""
+    lib = D.lib()
+    stream = torch.cuda.current_stream().cuda_stream
+    for t in TYPES:
+        g = np.random.default_rng(cols)
+        x, _ = make(g, (rows, cols), t)
+        other, _ = make(g, (rows, cols), t, pad)
+        drop = D.Drop(0.4, 6, 7)
+        want = D.dropout(x, drop, other)
+        y = x.clone()
+        lib.dropout(rows, cols, {"f32": D.F32, "bf16": D.BF16, "f16": D.F16}[t], y.data_ptr(), cols, other.data_ptr(),
+                    other.stride(0), drop._c, y.data_ptr(), stream)
+        assert torch.equal(y, want)
+        y = x.clone()                                  # onto the residual
+        want = D.dropout(other, drop, x)
+        lib.dropout(rows, cols, {"f32": D.F32, "bf16": D.BF16, "f16": D.F16}[t], other.data_ptr(), other.stride(0),
+                    y.data_ptr(), cols, drop._c, y.data_ptr(), stream)
+        assert torch.equal(y, want)
+
+
 def test_dropout_counter_is_added_to_the_offset():
     x = torch.randn(1000, device="cuda")
     c = torch.tensor([5], device="cuda")

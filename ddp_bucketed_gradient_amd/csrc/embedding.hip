@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void lookup_kernel(Lookup a) {
 //     its units, and
 //  3. a last kernel adds those up.
 //
-// BERT-large (16384 tokens, 30522 x 1024 in fp32 from bf16): 41 us, of which the
+// BERT-large (16384 tokens, 30522 x 1024 in fp32 from bf16): 42 us, of which the
 // zeros beside the sort take 26 and floor at 25 on a copy's rate.
 struct Zeros {
   uint64_t at;        // 16-byte aligned

@@ -448,8 +448,8 @@ __global__ __launch_bounds__(kWeightCols * kWeightWaves) void norm_weights_kerne
 
 // ---------------------------------------------------------------------------
 // Dropout, with or without a residual: a group of eight elements to a lane,
-// counted row by row. Bound by HBM: 8192 x 8192 in bf16 46.5 us, 5.8 TB/s (with two
-// or four groups to a lane 46.3 and 48).
+// counted row by row. Bound by HBM: 8192 x 8192 in bf16 45 us, 6.0 TB/s (with two
+// or four groups to a lane 46 and 48).
 struct Drop {
   uint64_t x, residual, y;
   int64_t x_stride, residual_stride;   // in elements

@@ -326,6 +326,23 @@ def test_gradient_many_tiles_and_passes(n, vocab):
     grad_case(4, g.integers(0, vocab, n), vocab, 2, "f16", "f16", True)
 
 
+def test_gradient_millions_of_places():
+    """Units longer than 128 places, thousands of tiles, a run of half of the places."""
+    g = np.random.default_rng(3)
+    n, vocab = 9_000_001, 1000
+    tokens = g.integers(-1, vocab + 1, n)
+    tokens[g.random(n) < 0.5] = 77
+    dy, DY = make(g, (n, 1), "f32")
+    d, OLD = make(g, (vocab, 1), "f32")
+    D.embedding_backward(dy, torch.from_numpy(tokens).cuda(), d, 0.25, True)
+    inside = (tokens >= 0) & (tokens < vocab)
+    sums = lambda x: np.bincount(tokens[inside], x[inside, 0], vocab)[:, None]  # noqa: E731
+    want = 0.25 * sums(DY)
+    # deep: a unit's places one after the other (256), then the parts of the longest run, 4.5 M / 256 over 16 lanes
+    bound = (256 + 3 + 4_600_000 // 256 // 16 + 16) * OL.U * 0.25 * sums(np.abs(DY)) + OL.U * np.abs(want + OLD)
+    check(d, want + OLD, bound, "f32", "dtable")
+
+
 @pytest.mark.parametrize("offset", [0, 1, 3, 7])
 @pytest.mark.parametrize("gt", ["f32", "bf16"])
 def test_gradient_at_odd_addresses(offset, gt):

@@ -153,13 +153,15 @@ def _lib(lib):
 
 def dropout(x, drop: Drop, residual=None, lib: Optional[_abi.Lib] = None):
     """``x`` with a share of its elements dropped and the others scaled, plus
-    ``residual``. Contiguous, of x's type (fp32, bf16 or fp16); x itself where
-    nothing is dropped or added."""
+    ``residual``: a new contiguous tensor of x's type (fp32, bf16 or fp16). Where
+    nothing is dropped or added that is x itself, as it lies, and no copy."""
     code = _code(x.dtype, "x")
+    if residual is None and not drop.active:
+        if not x.is_cuda:
+            raise ValueError("x must be a CUDA tensor")
+        return x
     rows, cols, stride = _rows(x, "x")
     rs = 0 if residual is None else _rows(residual, "residual", x)[2]
-    if residual is None and not drop.active and x.is_contiguous():
-        return x
     y = _like(x)
     _call(x.device, _lib(lib).dropout, rows, cols, code, x.data_ptr(), stride,
           0 if residual is None else residual.data_ptr(), rs, drop._on(x.device), y.data_ptr())
@@ -167,7 +169,8 @@ def dropout(x, drop: Drop, residual=None, lib: Optional[_abi.Lib] = None):
 
 
 def dropout_backward(dy, drop: Drop, lib: Optional[_abi.Lib] = None):
-    """The gradient of dropout's x (the residual's is dy)."""
+    """The gradient of dropout's x (the residual's is dy): dy itself where nothing
+    is dropped."""
     return dropout(dy, drop, lib=lib)
 
 

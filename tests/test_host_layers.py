@@ -266,3 +266,15 @@ def test_rows_of_a_tensor(make, want):
             _rows(Fake(make()), "x")
     else:
         assert _rows(Fake(make()), "x") == want
+
+
+def test_where_nothing_is_dropped_or_added_x_itself_is_returned():
+    """No copy of rows that are cut out of a wider tensor either, in both directions."""
+    for x in (torch.zeros(4, 6), torch.zeros(4, 9)[:, :6], torch.zeros(9, 4).t()):
+        f = Fake(x)
+        assert D.dropout(f, D.Drop(0.0, 1)) is f and D.dropout_backward(f, D.Drop(2.0 ** -18, 1)) is f
+    double = Fake(torch.zeros(4, 6))
+    double.dtype = torch.float64
+    for x in (torch.zeros(4, 6), double):
+        with pytest.raises(ValueError):
+            D.dropout(x, D.Drop(0.0, 1))

@@ -44,7 +44,8 @@ SYMBOLS = [
     "ddpb_adamw_set_step", "ddpb_adamw_get_step",
     "ddpb_check_writable", "ddpb_dropout", "ddpb_layer_norm", "ddpb_layer_norm_backward",
     "ddpb_layer_norm_backward_workspace_bytes", "ddpb_embedding", "ddpb_embedding_backward",
-    "ddpb_embedding_backward_workspace_bytes",
+    "ddpb_embedding_backward_workspace_bytes", "ddpb_layer_norm_backward_check",
+    "ddpb_embedding_backward_check",
 ]
 
 
@@ -125,6 +126,8 @@ def _sig(lib):
         "ddpb_embedding_backward": [i64, vp, i32, i64, i64, vp, i64, i32, f64, vp, i32, i32, vp, i64, vp],
         "ddpb_last_error": [],
     }
+    for name in ("ddpb_layer_norm_backward", "ddpb_embedding_backward"):     # all but the stream
+        S[name + "_check"] = S[name][:-1]
     for name, args in S.items():
         f = getattr(lib, name)
         f.argtypes = args
@@ -343,6 +346,13 @@ class Lib:
         if rc != OK:
             raise DdpbError(rc, self.last_error())
 
+    def layer_norm_backward_check(self, rows, cols, dtype, dy, dy_stride, h, h_stride, stats, grad_h, grad_h_stride,
+                                  drop, weight, weight_dtype, dh, dx, dweight, dbias, grad_dtype, accumulate,
+                                  workspace, ws_bytes):
+        self._check(self.dll.ddpb_layer_norm_backward_check(
+            rows, cols, dtype, dy, dy_stride, h, h_stride, stats, grad_h, grad_h_stride, drop, weight, weight_dtype,
+            dh, dx, dweight, dbias, grad_dtype, 1 if accumulate else 0, workspace, ws_bytes))
+
     def embedding(self, n, tokens, token_bytes, vocab, cols, table, table_dtype, scale, residual, residual_stride, y,
                   dtype, stream):
         rc = self.dll.ddpb_embedding(n, tokens, token_bytes, vocab, cols, table, table_dtype, scale, residual,
@@ -361,6 +371,12 @@ class Lib:
                                               dtable, grad_dtype, 1 if accumulate else 0, workspace, ws_bytes, stream)
         if rc != OK:
             raise DdpbError(rc, self.last_error())
+
+    def embedding_backward_check(self, n, tokens, token_bytes, vocab, cols, dy, dy_stride, dtype, scale, dtable,
+                                 grad_dtype, accumulate, workspace, ws_bytes):
+        self._check(self.dll.ddpb_embedding_backward_check(
+            n, tokens, token_bytes, vocab, cols, dy, dy_stride, dtype, scale, dtable, grad_dtype,
+            1 if accumulate else 0, workspace, ws_bytes))
 
     # -- diagnostics ------------------------------------------------------------------
     def get_launch_log(self, h, with_stamps: bool = False):

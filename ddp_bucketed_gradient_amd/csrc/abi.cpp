@@ -67,14 +67,14 @@ int guarded(const char* what, F f) {
   }
 }
 
-// Builds the kernels' arguments, checks them and enqueues the call.
+// Builds the kernels' arguments, checks them and enqueues the call (if there is one).
 template <typename Args, typename Fill>
 int enqueue(const char* what, int (ddpb::LayersDevice::*call)(const Args&, std::string*), Fill fill) {
   return guarded(what, [&](std::string* err) {
     Args a;
     int rc = fill(&a, err);
     if (rc == DDPB_OK) rc = ddpb::check(a, err);
-    return rc == DDPB_OK ? (ddpb::layers_device()->*call)(a, err) : rc;
+    return rc == DDPB_OK && call != nullptr ? (ddpb::layers_device()->*call)(a, err) : rc;
   });
 }
 
@@ -82,6 +82,62 @@ int drop_of(const ddpb_drop* d, ddpb::DropSpec* out, const char* what, std::stri
   if (d == nullptr) return DDPB_OK;
   const ddpb::DropArgs a{d->p, d->seed, d->offset, d->offset_device};
   return ddpb::make_drop(&a, out, what, err);
+}
+
+typedef int (ddpb::LayersDevice::*NormBackwardCall)(const ddpb::NormBackwardArgs&, std::string*);
+typedef int (ddpb::LayersDevice::*LookupBackwardCall)(const ddpb::LookupBackwardArgs&, std::string*);
+
+int norm_backward(NormBackwardCall call, int64_t rows, int64_t cols, int32_t dtype, ddpb::Matrix dy, ddpb::Matrix h,
+                  const float* stats, ddpb::Matrix grad_h, const ddpb_drop* drop, const void* weight,
+                  int32_t weight_dtype, void* dh, void* dx, void* dweight, void* dbias, int32_t grad_dtype,
+                  int32_t accumulate, void* workspace, int64_t ws_bytes, void* stream) {
+  if (!is_dtype(dtype) || !is_dtype(weight_dtype) || !is_dtype(grad_dtype))
+    return fail(DDPB_E_ARG, "layer_norm_backward: bad dtype");
+  return enqueue("layer_norm_backward", call, [&](ddpb::NormBackwardArgs* a, std::string* err) {
+    a->rows = rows;
+    a->cols = cols;
+    a->dtype = dtype;
+    a->weight_dtype = weight_dtype;
+    a->grad_dtype = grad_dtype;
+    a->dy = dy;
+    a->h = h;
+    a->grad_h = grad_h;
+    a->stats = stats;
+    a->weight = weight;
+    a->dh = dh;
+    a->dx = dx;
+    a->dweight = dweight;
+    a->dbias = dbias;
+    a->accumulate = accumulate != 0;
+    a->workspace = workspace;
+    a->ws_bytes = ws_bytes;
+    a->stream = stream;
+    return drop_of(drop, &a->drop, "layer_norm_backward", err);
+  });
+}
+
+int embedding_backward(LookupBackwardCall call, int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab,
+                       int64_t cols, ddpb::Matrix dy, int32_t dtype, double scale, void* dtable, int32_t grad_dtype,
+                       int32_t accumulate, void* workspace, int64_t ws_bytes, void* stream) {
+  if (!is_dtype(dtype) || !is_dtype(grad_dtype) || (token_bytes != 4 && token_bytes != 8))
+    return fail(DDPB_E_ARG, "embedding_backward: bad dtype or token_bytes");
+  return enqueue("embedding_backward", call, [&](ddpb::LookupBackwardArgs* a, std::string*) {
+    a->n = n;
+    a->vocab = vocab;
+    a->cols = cols;
+    a->tokens = tokens;
+    a->token_bytes = token_bytes;
+    a->dy = dy;
+    a->dtype = dtype;
+    a->grad_dtype = grad_dtype;
+    a->scale = static_cast<float>(scale);
+    a->dtable = dtable;
+    a->accumulate = accumulate != 0;
+    a->workspace = workspace;
+    a->ws_bytes = ws_bytes;
+    a->stream = stream;
+    return DDPB_OK;
+  });
 }
 }  // namespace
 
@@ -570,30 +626,19 @@ int ddpb_layer_norm_backward(int64_t rows, int64_t cols, int32_t dtype, const vo
                              int64_t grad_h_stride, const ddpb_drop* drop, const void* weight, int32_t weight_dtype,
                              void* dh, void* dx, void* dweight, void* dbias, int32_t grad_dtype, int32_t accumulate,
                              void* workspace, int64_t ws_bytes, void* stream) {
-  if (!is_dtype(dtype) || !is_dtype(weight_dtype) || !is_dtype(grad_dtype))
-    return fail(DDPB_E_ARG, "layer_norm_backward: bad dtype");
-  return enqueue("layer_norm_backward", &ddpb::LayersDevice::norm_backward,
-                 [&](ddpb::NormBackwardArgs* a, std::string* err) {
-    a->rows = rows;
-    a->cols = cols;
-    a->dtype = dtype;
-    a->weight_dtype = weight_dtype;
-    a->grad_dtype = grad_dtype;
-    a->dy = {dy, dy_stride};
-    a->h = {h, h_stride};
-    a->grad_h = {grad_h, grad_h_stride};
-    a->stats = stats;
-    a->weight = weight;
-    a->dh = dh;
-    a->dx = dx;
-    a->dweight = dweight;
-    a->dbias = dbias;
-    a->accumulate = accumulate != 0;
-    a->workspace = workspace;
-    a->ws_bytes = ws_bytes;
-    a->stream = stream;
-    return drop_of(drop, &a->drop, "layer_norm_backward", err);
-  });
+  return norm_backward(&ddpb::LayersDevice::norm_backward, rows, cols, dtype, {dy, dy_stride}, {h, h_stride}, stats,
+                       {grad_h, grad_h_stride}, drop, weight, weight_dtype, dh, dx, dweight, dbias, grad_dtype,
+                       accumulate, workspace, ws_bytes, stream);
+}
+
+int ddpb_layer_norm_backward_check(int64_t rows, int64_t cols, int32_t dtype, const void* dy, int64_t dy_stride,
+                                   const void* h, int64_t h_stride, const float* stats, const void* grad_h,
+                                   int64_t grad_h_stride, const ddpb_drop* drop, const void* weight,
+                                   int32_t weight_dtype, void* dh, void* dx, void* dweight, void* dbias,
+                                   int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t ws_bytes) {
+  return norm_backward(nullptr, rows, cols, dtype, {dy, dy_stride}, {h, h_stride}, stats, {grad_h, grad_h_stride}, drop,
+                       weight, weight_dtype, dh, dx, dweight, dbias, grad_dtype, accumulate, workspace, ws_bytes,
+                       nullptr);
 }
 
 int ddpb_dropout(int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
@@ -644,26 +689,15 @@ int ddpb_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t co
 int ddpb_embedding_backward(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols,
                             const void* dy, int64_t dy_stride, int32_t dtype, double scale, void* dtable,
                             int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t ws_bytes, void* stream) {
-  if (!is_dtype(dtype) || !is_dtype(grad_dtype) || (token_bytes != 4 && token_bytes != 8))
-    return fail(DDPB_E_ARG, "embedding_backward: bad dtype or token_bytes");
-  return enqueue("embedding_backward", &ddpb::LayersDevice::lookup_backward,
-                 [&](ddpb::LookupBackwardArgs* a, std::string*) {
-    a->n = n;
-    a->vocab = vocab;
-    a->cols = cols;
-    a->tokens = tokens;
-    a->token_bytes = token_bytes;
-    a->dy = {dy, dy_stride};
-    a->dtype = dtype;
-    a->grad_dtype = grad_dtype;
-    a->scale = static_cast<float>(scale);
-    a->dtable = dtable;
-    a->accumulate = accumulate != 0;
-    a->workspace = workspace;
-    a->ws_bytes = ws_bytes;
-    a->stream = stream;
-    return DDPB_OK;
-  });
+  return embedding_backward(&ddpb::LayersDevice::lookup_backward, n, tokens, token_bytes, vocab, cols, {dy, dy_stride},
+                            dtype, scale, dtable, grad_dtype, accumulate, workspace, ws_bytes, stream);
+}
+
+int ddpb_embedding_backward_check(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols,
+                                  const void* dy, int64_t dy_stride, int32_t dtype, double scale, void* dtable,
+                                  int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t ws_bytes) {
+  return embedding_backward(nullptr, n, tokens, token_bytes, vocab, cols, {dy, dy_stride}, dtype, scale, dtable,
+                            grad_dtype, accumulate, workspace, ws_bytes, nullptr);
 }
 
 }  // extern "C"

@@ -194,7 +194,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, drop
 
 
 def _norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulate, lib):
-    """layer_norm_backward in two steps: the checks, and what they return, the call."""
+    """layer_norm_backward in steps: the checks here return the device, the bytes of the
+    workspace and prepare(workspace, check), which allocates the outputs, has the library
+    check the call as well, if so asked, and returns it. All but the call itself writes nothing."""
     torch = _t()
     code, dev = _code(dy.dtype, "dy"), dy.device
     rows, cols, stride = _rows(dy, "dy")
@@ -209,19 +211,44 @@ def _norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulat
     dropped = drop is not None and drop.active
     spec = drop._on(dev) if dropped else None
     lib = _lib(lib)
+    nbytes = lib.layer_norm_backward_workspace_bytes(rows, cols) if dw or db else 0
 
-    def run():
-        nbytes = lib.layer_norm_backward_workspace_bytes(rows, cols) if dw or db else 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    def prepare(ws, check):
         dh = _like(dy)
         dx = _like(dy) if dropped else dh
-        _call(dev, lib.layer_norm_backward, rows, cols, code, dy.data_ptr(), stride, h.data_ptr(), hs, st,
-              0 if grad_h is None else grad_h.data_ptr(), gs, spec, w, wc, dh.data_ptr(),
-              dx.data_ptr() if dropped else 0, dw, db, gc, accumulate, 0 if ws is None else ws.data_ptr(),
-              nbytes)
-        _wrote(dweight, dbias)
-        return NormGrads(dx, dh)
-    return run
+        args = (rows, cols, code, dy.data_ptr(), stride, h.data_ptr(), hs, st,
+                0 if grad_h is None else grad_h.data_ptr(), gs, spec, w, wc, dh.data_ptr(),
+                dx.data_ptr() if dropped else 0, dw, db, gc, accumulate, 0 if ws is None else ws.data_ptr(), nbytes)
+        if check:
+            lib.layer_norm_backward_check(*args)
+
+        def run():
+            _call(dev, lib.layer_norm_backward, *args)
+            _wrote(dweight, dbias)
+            return NormGrads(dx, dh)
+        return run
+    return dev, nbytes, prepare
+
+
+def _workspace(device, nbytes):
+    return _t().empty(nbytes, dtype=_t().uint8, device=device) if nbytes else None
+
+
+def _alone(device, nbytes, prepare):
+    """A backward pass by itself."""
+    ws = _workspace(device, nbytes)
+    return prepare(ws, False)()
+
+
+def _together(passes):
+    """The calls of several backward passes, all of them with their memory and checked
+    by the library, and the workspaces, which have to be kept until they have been made.
+    Passes on one device share one: they run one after the other on one stream."""
+    most = {}
+    for device, nbytes, _ in passes:
+        most[device] = max(most.get(device, 0), nbytes)
+    ws = {device: _workspace(device, nbytes) for device, nbytes in most.items()}
+    return [prepare(ws[device], True) for device, _, prepare in passes], ws
 
 
 def layer_norm_backward(dy, h, stats, weight=None, dweight=None, dbias=None, grad_h=None,
@@ -232,7 +259,7 @@ def layer_norm_backward(dy, h, stats, weight=None, dweight=None, dbias=None, gra
     wanted; one type): written, or with ``accumulate`` added to. ``grad_h``: a
     gradient that reaches h from elsewhere, as where h itself goes on as the
     next residual."""
-    return _norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulate, lib)()
+    return _alone(*_norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulate, lib))
 
 
 def _tokens(tokens, device):
@@ -266,8 +293,7 @@ def embedding(tokens, table, scale: float = 1.0, residual=None, dtype=None, lib:
 
 
 def _embedding_backward(dy, tokens, dtable, scale, accumulate, lib):
-    """embedding_backward in two steps: the checks, and what they return, the call."""
-    torch = _t()
+    """embedding_backward in the steps of _norm_backward."""
     vocab, cols, gc = _table(dtable, "dtable")
     dev = dtable.device
     n, at, size = _tokens(tokens, dev)
@@ -276,14 +302,20 @@ def _embedding_backward(dy, tokens, dtable, scale, accumulate, lib):
     stride = _rows(dy, "dy")[2]
     code = _code(dy.dtype, "dy")
     lib = _lib(lib)
+    nbytes = lib.embedding_backward_workspace_bytes(n, vocab, cols)
 
-    def run():
-        ws = torch.empty(lib.embedding_backward_workspace_bytes(n, vocab, cols), dtype=torch.uint8, device=dev)
-        _call(dev, lib.embedding_backward, n, at, size, vocab, cols, dy.data_ptr(), stride, code, scale,
-              dtable.data_ptr(), gc, accumulate, ws.data_ptr(), ws.numel())
-        _wrote(dtable)
-        return dtable
-    return run
+    def prepare(ws, check):
+        args = (n, at, size, vocab, cols, dy.data_ptr(), stride, code, scale, dtable.data_ptr(), gc, accumulate,
+                ws.data_ptr(), nbytes)
+        if check:
+            lib.embedding_backward_check(*args)
+
+        def run():
+            _call(dev, lib.embedding_backward, *args)
+            _wrote(dtable)
+            return dtable
+        return run
+    return dev, nbytes, prepare
 
 
 def embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bool = False,
@@ -292,4 +324,4 @@ def embedding_backward(dy, tokens, dtable, scale: float = 1.0, accumulate: bool 
     ``dtable`` becomes ``scale`` times the sum of dy over the places of token v,
     in their order; with ``accumulate`` that is added to it. Tokens outside of the
     table are left out. Returns dtable."""
-    return _embedding_backward(dy, tokens, dtable, scale, accumulate, lib)()
+    return _alone(*_embedding_backward(dy, tokens, dtable, scale, accumulate, lib))

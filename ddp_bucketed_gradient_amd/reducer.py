@@ -272,13 +272,23 @@ class Reducer:
         for v in vs:
             self.lib.check_writable(self.h, v)
 
+    def _write(self, vs, passes):
+        """Runs backward passes that write the variables vs. What can refuse them, of any
+        replica, comes before the first write."""
+        calls, ws = _layers._together(passes)
+        out = [call() for call in calls]
+        del ws
+        self.lib.mark_ready_many(self.h, vs)
+        return out
+
     def layer_norm_backward(self, weight_var: Optional[int], bias_var: Optional[int], dy, h, stats, weight=None,
                             grad_h=None, drop=None, accumulate: bool = False):
         """layer_norm_backward for all replicas, the weights' gradients into
         the bound tensors of variables ``weight_var`` and ``bias_var`` (None for
         a norm without), which are then marked ready, the bias first. ``dy``,
         ``h``, ``stats`` and, if given, ``weight``, ``grad_h`` and ``drop`` hold one
-        entry for each replica. ``accumulate``: add to the local steps before.
+        entry for each replica, none of which overlaps these variables' gradients
+        (of any replica). ``accumulate``: add to the local steps before.
         Returns a NormGrads for each replica. On the compute stream, which has
         to be the current one."""
         every = lambda x: [None] * self.R if x is None else list(x)  # noqa: E731
@@ -288,11 +298,9 @@ class Reducer:
             raise ValueError("weight and bias are two variables")
         self._writable(vs, dy, h, stats, weight, grad_h, drop)
         to = lambda r, v: None if v is None else self._grads[r][v]  # noqa: E731
-        calls = [_layers._norm_backward(dy[r], h[r], stats[r], weight[r], to(r, weight_var), to(r, bias_var),
-                                        grad_h[r], drop[r], accumulate, self.lib) for r in range(self.R)]
-        out = [run() for run in calls]
-        self.lib.mark_ready_many(self.h, vs)
-        return out
+        return self._write(vs, [_layers._norm_backward(dy[r], h[r], stats[r], weight[r], to(r, weight_var),
+                                                       to(r, bias_var), grad_h[r], drop[r], accumulate, self.lib)
+                                for r in range(self.R)])
 
     def embedding_backward(self, v: int, dy, tokens, scale: float = 1.0, accumulate: bool = False):
         """embedding_backward for all replicas into the bound tensors of
@@ -301,10 +309,8 @@ class Reducer:
         self._writable([v], dy, tokens)
         if len(self.shapes[v]) != 2:
             raise ValueError(f"variable {v} has shape {self.shapes[v]}, not two dimensions")
-        for run in [_layers._embedding_backward(dy[r], tokens[r], self._grads[r][v].view(self.shapes[v]), scale,
-                                                accumulate, self.lib) for r in range(self.R)]:
-            run()
-        self.lib.mark_ready(self.h, v)
+        self._write([v], [_layers._embedding_backward(dy[r], tokens[r], self._grads[r][v].view(self.shapes[v]), scale,
+                                                      accumulate, self.lib) for r in range(self.R)])
 
     # -- after the synchronisation -------------------------------------------------------
     def _replica_grads(self):

@@ -592,6 +592,13 @@ int ddpb_layer_norm_backward(int64_t rows, int64_t cols, int32_t dtype, const vo
                              int64_t grad_h_stride, const ddpb_drop* drop, const void* weight, int32_t weight_dtype,
                              void* dh, void* dx, void* dweight, void* dbias, int32_t grad_dtype, int32_t accumulate,
                              void* workspace, int64_t ws_bytes, void* stream);
+/* All checks of that call and nothing else: a backward pass of several replicas is
+ * refused before it has written one. */
+int ddpb_layer_norm_backward_check(int64_t rows, int64_t cols, int32_t dtype, const void* dy, int64_t dy_stride,
+                                   const void* h, int64_t h_stride, const float* stats, const void* grad_h,
+                                   int64_t grad_h_stride, const ddpb_drop* drop, const void* weight,
+                                   int32_t weight_dtype, void* dh, void* dx, void* dweight, void* dbias,
+                                   int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t ws_bytes);
 
 /* y_i = scale * table[tokens[i]] + residual_i for n tokens of 4 or 8 bytes
  * (int32_t, int64_t); residual may be NULL. A token outside of 0 .. vocab - 1
@@ -608,6 +615,9 @@ int ddpb_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t co
 int ddpb_embedding_backward(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols,
                             const void* dy, int64_t dy_stride, int32_t dtype, double scale, void* dtable,
                             int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t ws_bytes, void* stream);
+int ddpb_embedding_backward_check(int64_t n, const void* tokens, int32_t token_bytes, int64_t vocab, int64_t cols,
+                                  const void* dy, int64_t dy_stride, int32_t dtype, double scale, void* dtable,
+                                  int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t ws_bytes);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics.

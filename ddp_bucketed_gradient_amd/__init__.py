@@ -45,6 +45,6 @@ for _n in ["reducer_create", "destroy", "num_buckets", "get_locator", "get_bucke
            "set_local_used", "set_sync_step", "bind_static",
            "norm_create", "norm_destroy", "norm_workspace_bytes", "norm_bind", "norm_compute",
            "adamw_create", "adamw_destroy", "adamw_workspace_bytes", "adamw_bind", "adamw_step",
-           "adamw_set_step", "adamw_get_step", "check_writable"]:
+           "adamw_set_step", "adamw_get_step", "check_writable", "begin_writes"]:
     globals()[_n] = _fwd(_n)
 del _n

@@ -44,7 +44,7 @@ SYMBOLS = [
     "ddpb_adamw_set_step", "ddpb_adamw_get_step",
     "ddpb_check_writable", "ddpb_dropout", "ddpb_layer_norm", "ddpb_layer_norm_backward",
     "ddpb_layer_norm_backward_workspace_bytes", "ddpb_embedding", "ddpb_embedding_backward",
-    "ddpb_embedding_backward_workspace_bytes", "ddpb_layer_norm_backward_check",
+    "ddpb_embedding_backward_workspace_bytes", "ddpb_begin_writes", "ddpb_layer_norm_backward_check",
     "ddpb_embedding_backward_check",
 ]
 
@@ -124,6 +124,7 @@ def _sig(lib):
         "ddpb_embedding": [i64, vp, i32, i64, i64, vp, i32, f64, vp, i64, vp, i32, vp],
         "ddpb_embedding_backward_workspace_bytes": [i64, i64, i64, P64],
         "ddpb_embedding_backward": [i64, vp, i32, i64, i64, vp, i64, i32, f64, vp, i32, i32, vp, i64, vp],
+        "ddpb_begin_writes": [vp, P32, i32],
         "ddpb_last_error": [],
     }
     for name in ("ddpb_layer_norm_backward", "ddpb_embedding_backward"):     # all but the stream
@@ -319,6 +320,9 @@ class Lib:
     # addresses are integers, 0 for NULL; drop: a DropStruct or None
     def check_writable(self, h, v: int):
         self._check(self.dll.ddpb_check_writable(h, v))
+
+    def begin_writes(self, h, vs: Sequence[int]):
+        self._check(self.dll.ddpb_begin_writes(h, (i32 * max(len(vs), 1))(*vs), len(vs)))
 
     def dropout(self, rows, cols, dtype, x, x_stride, residual, residual_stride, drop, y, stream):
         rc = self.dll.ddpb_dropout(rows, cols, dtype, x, x_stride, residual, residual_stride, drop, y, stream)

@@ -592,6 +592,12 @@ int ddpb_check_writable(ddpb_t h, int32_t v) {
   return pass(h->red.check_writable(v, &err), err);
 }
 
+int ddpb_begin_writes(ddpb_t h, const int32_t* vs, int32_t n) {
+  if (!h || n < 0 || (n > 0 && !vs)) return fail(DDPB_E_ARG, "begin_writes: bad argument");
+  std::string err;
+  return pass(h->red.begin_writes(vs, n, &err), err);
+}
+
 int ddpb_layer_norm(int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
                     int64_t residual_stride, const ddpb_drop* drop, const void* weight, const void* bias,
                     int32_t weight_dtype, double eps, void* y, void* h, float* stats, void* stream) {

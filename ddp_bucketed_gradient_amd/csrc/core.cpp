@@ -122,6 +122,15 @@ int Reducer::check_writable(int32_t v, std::string* err) const {
   return kOk;
 }
 
+int Reducer::begin_writes(const int32_t* vs, int32_t n, std::string* err) {
+  for (int32_t i = 0; i < n; ++i) {
+    const int rc = check_writable(vs[i], err);
+    if (rc != kOk) return rc;
+  }
+  if (n > 0) averaged_ = false;
+  return kOk;
+}
+
 int Reducer::mark_ready(int32_t v, std::string* err) {
   if (!bound_) {
     *err = "mark_ready: reducer is not bound";

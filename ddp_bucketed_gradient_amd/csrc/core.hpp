@@ -199,6 +199,9 @@ class Reducer {
   // unused in it, kErrIndex, kErrIncomplete while a failed iteration is latched,
   // kErrDoubleReady once v is ready (its bucket may be reducing).
   int check_writable(int32_t v, std::string* err) const;
+  // The same for several, which are about to be written: from here to the next
+  // synchronisation the gradients are not averaged, whether the hooks run or not.
+  int begin_writes(const int32_t* vs, int32_t n, std::string* err);
 
  private:
   void begin_iteration();

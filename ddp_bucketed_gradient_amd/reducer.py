@@ -274,8 +274,10 @@ class Reducer:
 
     def _write(self, vs, passes):
         """Runs backward passes that write the variables vs. What can refuse them, of any
-        replica, comes before the first write."""
+        replica, comes before the first write; a call that fails behind it leaves
+        gradients that do not count as averaged."""
         calls, ws = _layers._together(passes)
+        self.lib.begin_writes(self.h, vs)
         out = [call() for call in calls]
         del ws
         self.lib.mark_ready_many(self.h, vs)

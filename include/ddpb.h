@@ -283,6 +283,11 @@ int ddpb_mark_ready_many(ddpb_t h, const int32_t* vs, int32_t n);
  * failure), DDPB_E_DOUBLE_READY (marked ready already: its bucket may be reducing). */
 int ddpb_check_writable(ddpb_t h, int32_t v);
 
+/* The same for n variables, whose gradients a backward pass writes next: from here
+ * to the next synchronisation they do not count as averaged (ddpb_norm_compute and
+ * ddpb_adamw_step refuse them), even if the pass fails before its hooks. */
+int ddpb_begin_writes(ddpb_t h, const int32_t* vs, int32_t n);
+
 /* End of backward: every bucket must have been launched (else
  * DDPB_E_INCOMPLETE, latched; the compute stream is then still made to wait
  * for the buckets that did launch). Records a completion event on every side

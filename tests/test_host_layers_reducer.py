@@ -115,6 +115,52 @@ def test_no_memory_leaves_every_replica_unwritten(red, norm, monkeypatch):
     assert red.calls == [] and norm()
 
 
+@pytest.mark.parametrize("local", [False, True])
+def test_a_pass_that_fails_half_way_leaves_gradients_that_are_not_averaged(red, norm, monkeypatch, local):
+    if local:
+        red.set_sync(False)
+    real = layers._call
+    runs = []
+
+    def call(device, f, *args):
+        runs.append(f)
+        if len(runs) == 2:
+            raise D.DdpbError(D.E_HIP, "launch")
+        return real(device, f, *args)
+    monkeypatch.setattr(layers, "_call", call)
+    assert norm()
+    with pytest.raises(D.DdpbError):
+        red.embedding_backward(0, rows(), tokens())
+    assert not norm()
+    red.set_sync(True)
+    red.embedding_backward(0, rows(), tokens())            # written anew, no hook has run
+    red.layer_norm_backward(1, 2, rows(), rows(), stats())
+    red.finalize()
+    assert norm()
+
+
+def test_begin_writes(red, norm):
+    lib = red.lib
+    for vs, code in (([0, 3], D.E_INDEX), ([-1], D.E_INDEX)):
+        with pytest.raises(D.DdpbError) as e:
+            lib.begin_writes(red.h, vs)
+        assert e.value.code == code and norm()
+    lib.begin_writes(red.h, [])
+    assert norm()
+    red.mark_ready(1)
+    with pytest.raises(D.DdpbError) as e:
+        lib.begin_writes(red.h, [0, 1])
+    assert e.value.code == D.E_DOUBLE_READY
+    red.mark_ready_many([0, 2])
+    red.finalize()
+    assert norm()
+    lib.begin_writes(red.h, [0, 1, 2])
+    assert not norm()
+    assert lib.dll.ddpb_begin_writes(None, None, 0) == D.E_ARG
+    assert lib.dll.ddpb_begin_writes(red.h, None, 1) == D.E_ARG
+    assert lib.dll.ddpb_begin_writes(red.h, None, -1) == D.E_ARG
+
+
 def test_the_checks_are_those_of_the_calls(red):
     from test_host_layers import LOOK_B, NORM_B
     lib = red.lib

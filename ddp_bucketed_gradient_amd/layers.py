@@ -33,7 +33,10 @@ def _t():
 class Drop:
     """Which elements a dropout keeps: a function of the seed, the offset and an
     element's index, so that nothing is stored for the backward pass, which
-    takes the same Drop. Each dropout of a step needs an offset of its own.
+    takes the same Drop. Two dropouts with one seed have one mask where their
+    offsets, the counters included, are equal: no two, of any step, may be. With
+    a counter of steps that is ``Drop(p, seed, offset=site << 32, counter=step)``,
+    site numbering the dropouts of a step.
 
     ``p``: the share that is dropped, rounded to a multiple of 2^-16 (what is
     kept is scaled by just that share). ``counter``: None, or a 1-element int64

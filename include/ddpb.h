@@ -558,7 +558,10 @@ int ddpb_adamw_get_step(ddpb_adamw_t a, int64_t* step);
  * rounds of the counter (i / 8, offset + *offset_device), two 64-bit numbers,
  * lower words first, under the key `seed`. Nothing is stored for the backward
  * pass, which is the same map of the gradient: pass it the same ddpb_drop. Two
- * dropouts of one step need offsets (or seeds) of their own. */
+ * dropouts with the same seed and the same sum offset + *offset_device drop the
+ * same elements, in whichever steps they are: with a number that counts steps in
+ * device memory, the offsets of a step's dropouts lie further apart than it will
+ * ever count (dropout k: k << 32), or their seeds differ. */
 typedef struct ddpb_drop {
   double p;                       /* in [0, 1] */
   uint64_t seed;

@@ -278,3 +278,24 @@ def test_where_nothing_is_dropped_or_added_x_itself_is_returned():
     for x in (torch.zeros(4, 6), double):
         with pytest.raises(ValueError):
             D.dropout(x, D.Drop(0.0, 1))
+
+
+def test_dropouts_used_as_documented_never_share_a_mask():
+    """The offset that the documentation gives a place, plus the step's counter, over
+    places and steps; and that the masks of such sums differ."""
+    import os
+    import re
+
+    from oracle import layers as OL
+    here = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(here, "README.md")) as f:
+        texts = [f.read(), D.Drop.__doc__]
+    for text in texts:
+        forms = re.findall(r"Drop\([^()]*offset=([^,()]+),\s*counter=step\)", text)
+        assert forms
+        for form in forms:
+            steps = (0, 1, 2, 3, 19, 1 << 20, (1 << 32) - 1)
+            at = [eval(form, {"site": site}) + step for site in range(20) for step in steps]
+            assert len(set(at)) == len(at)
+    masks = {tuple(OL.random16(0, 64, 1, (site << 32) + step) < 6554) for site in range(8) for step in range(8)}
+    assert len(masks) == 64

@@ -7,7 +7,8 @@ the native library. The functions work like torch's own: on the current stream
 of the tensors' device, with outputs and workspaces from torch's allocator, so
 they can be captured into graphs. They record nothing for autograd: the backward
 passes are called by name and write the parameters' gradients where they are
-told to, such as the tensors a Reducer is bound to.
+told to, such as the tensors a Reducer is bound to. Where autograd is recording,
+inputs that require a gradient are therefore refused: their results would not.
 """
 from __future__ import annotations
 
@@ -126,6 +127,15 @@ def _vector(t, what: str, n: int, device, dtype=None):
     return t.data_ptr()
 
 
+def _unrecorded(*ts):
+    """Refuses inputs whose gradients would be lost without a word."""
+    if _t().is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                raise ValueError("an input requires a gradient, and autograd records nothing of this call: make it "
+                                 "under torch.no_grad() and call the backward pass by name, or pass a detached tensor")
+
+
 def _call(device, f, *args):
     """f(*args, stream) on the current stream of ``device``."""
     torch = _t()
@@ -163,6 +173,7 @@ def dropout(x, drop: Drop, residual=None, lib: Optional[_abi.Lib] = None):
         if not x.is_cuda:
             raise ValueError("x must be a CUDA tensor")
         return x
+    _unrecorded(x, residual)
     rows, cols, stride = _rows(x, "x")
     rs = 0 if residual is None else _rows(residual, "residual", x)[2]
     y = _like(x)
@@ -181,6 +192,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, drop
                lib: Optional[_abi.Lib] = None) -> Normed:
     """Layer norm over the last dimension of ``h = residual + dropout(x)``, in
     one pass. ``weight`` and ``bias``: one type, which may differ from x's."""
+    _unrecorded(x, weight, bias, residual)
     code, dev = _code(x.dtype, "x"), x.device
     rows, cols, stride = _rows(x, "x")
     rs = 0 if residual is None else _rows(residual, "residual", x)[2]
@@ -201,6 +213,7 @@ def _norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulat
     workspace and prepare(workspace, check), which allocates the outputs, has the library
     check the call as well, if so asked, and returns it. All but the call itself writes nothing."""
     torch = _t()
+    _unrecorded(dy, h, grad_h)
     code, dev = _code(dy.dtype, "dy"), dy.device
     rows, cols, stride = _rows(dy, "dy")
     hs = _rows(h, "h", dy)[2]
@@ -283,6 +296,7 @@ def _table(t, what: str):
 def embedding(tokens, table, scale: float = 1.0, residual=None, dtype=None, lib: Optional[_abi.Lib] = None):
     """``scale * table[tokens] + residual``, of the table's type or ``dtype``. A
     token outside of the table gives a row of zeros."""
+    _unrecorded(table, residual)
     vocab, cols, tc = _table(table, "table")
     dev = table.device
     n, at, size = _tokens(tokens, dev)
@@ -297,6 +311,7 @@ def embedding(tokens, table, scale: float = 1.0, residual=None, dtype=None, lib:
 
 def _embedding_backward(dy, tokens, dtable, scale, accumulate, lib):
     """embedding_backward in the steps of _norm_backward."""
+    _unrecorded(dy)
     vocab, cols, gc = _table(dtable, "dtable")
     dev = dtable.device
     n, at, size = _tokens(tokens, dev)

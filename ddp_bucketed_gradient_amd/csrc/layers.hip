@@ -110,9 +110,9 @@ __device__ __forceinline__ v8f input8(const Forward& a, uint32_t row, const Grou
 // The sum of a group's own elements.
 template <int EDGE>
 __device__ __forceinline__ float total(v8f x, const Group& g) {
-  if (EDGE == kShifted) {
+  if (EDGE != kWhole) {   // (the last element of a shifted group is always its own)
 #pragma unroll
-    for (int j = 0; j < 7; ++j) x[j] = own<EDGE>(g, j) ? x[j] : 0.0f;
+    for (int j = 0; j < (EDGE == kShifted ? 7 : 8); ++j) x[j] = own<EDGE>(g, j) ? x[j] : 0.0f;
   }
   return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
@@ -321,7 +321,8 @@ __global__ __launch_bounds__(norm_back_threads(LANES)) void norm_backward_kernel
       dw[k] = fma8(d, n, dw[k]);
       db[k] = db[k] + d;
       s[0] += total<EDGE>(x, g[k]);
-      s[1] += total<EDGE>(x * n, g[k]);
+      // a lane without columns holds n = -mean rstd, which may be infinite, and x = 0
+      s[1] += g[k].left > 0 ? total<EDGE>(x * n, g[k]) : 0.0f;
     }
     row_sum<LANES>(s, lds[turn]);
     s[0] *= inverse;

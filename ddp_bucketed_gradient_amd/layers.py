@@ -127,13 +127,15 @@ def _vector(t, what: str, n: int, device, dtype=None):
     return t.data_ptr()
 
 
-def _unrecorded(*ts):
-    """Refuses inputs whose gradients would be lost without a word."""
+def _wanted(t):
+    return t is not None and t.requires_grad
+
+
+def _unrecorded():
+    """Refuses inputs that require a gradient, which would be lost without a word."""
     if _t().is_grad_enabled():
-        for t in ts:
-            if t is not None and t.requires_grad:
-                raise ValueError("an input requires a gradient, and autograd records nothing of this call: make it "
-                                 "under torch.no_grad() and call the backward pass by name, or pass a detached tensor")
+        raise ValueError("an input requires a gradient, and autograd records nothing of this call: make it under "
+                         "torch.no_grad() and call the backward pass by name, or pass a detached tensor")
 
 
 def _call(device, f, *args):
@@ -173,7 +175,8 @@ def dropout(x, drop: Drop, residual=None, lib: Optional[_abi.Lib] = None):
         if not x.is_cuda:
             raise ValueError("x must be a CUDA tensor")
         return x
-    _unrecorded(x, residual)
+    if x.requires_grad or _wanted(residual):
+        _unrecorded()
     rows, cols, stride = _rows(x, "x")
     rs = 0 if residual is None else _rows(residual, "residual", x)[2]
     y = _like(x)
@@ -192,7 +195,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, drop
                lib: Optional[_abi.Lib] = None) -> Normed:
     """Layer norm over the last dimension of ``h = residual + dropout(x)``, in
     one pass. ``weight`` and ``bias``: one type, which may differ from x's."""
-    _unrecorded(x, weight, bias, residual)
+    if x.requires_grad or _wanted(weight) or _wanted(bias) or _wanted(residual):
+        _unrecorded()
     code, dev = _code(x.dtype, "x"), x.device
     rows, cols, stride = _rows(x, "x")
     rs = 0 if residual is None else _rows(residual, "residual", x)[2]
@@ -213,7 +217,8 @@ def _norm_backward(dy, h, stats, weight, dweight, dbias, grad_h, drop, accumulat
     workspace and prepare(workspace, check), which allocates the outputs, has the library
     check the call as well, if so asked, and returns it. All but the call itself writes nothing."""
     torch = _t()
-    _unrecorded(dy, h, grad_h)
+    if dy.requires_grad or h.requires_grad or _wanted(grad_h):
+        _unrecorded()
     code, dev = _code(dy.dtype, "dy"), dy.device
     rows, cols, stride = _rows(dy, "dy")
     hs = _rows(h, "h", dy)[2]
@@ -296,7 +301,8 @@ def _table(t, what: str):
 def embedding(tokens, table, scale: float = 1.0, residual=None, dtype=None, lib: Optional[_abi.Lib] = None):
     """``scale * table[tokens] + residual``, of the table's type or ``dtype``. A
     token outside of the table gives a row of zeros."""
-    _unrecorded(table, residual)
+    if table.requires_grad or _wanted(residual):
+        _unrecorded()
     vocab, cols, tc = _table(table, "table")
     dev = table.device
     n, at, size = _tokens(tokens, dev)
@@ -311,7 +317,8 @@ def embedding(tokens, table, scale: float = 1.0, residual=None, dtype=None, lib:
 
 def _embedding_backward(dy, tokens, dtable, scale, accumulate, lib):
     """embedding_backward in the steps of _norm_backward."""
-    _unrecorded(dy)
+    if dy.requires_grad:
+        _unrecorded()
     vocab, cols, gc = _table(dtable, "dtable")
     dev = dtable.device
     n, at, size = _tokens(tokens, dev)

@@ -60,7 +60,7 @@ class Drop:
             at = counter.data_ptr()
         m = (1 << 64) - 1
         self.p, self.seed, self.offset, self.counter = p, int(seed), int(offset), counter
-        self.active = _math.floor(p * 65536 + 0.5) > 0
+        self.active = p * 65536 >= 0.5
         self._c = _abi.DropStruct(p, self.seed & m, self.offset & m, at)
 
     def _on(self, device):

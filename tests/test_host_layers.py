@@ -299,3 +299,18 @@ def test_dropouts_used_as_documented_never_share_a_mask():
             assert len(set(at)) == len(at)
     masks = {tuple(OL.random16(0, 64, 1, (site << 32) + step) < 6554) for site in range(8) for step in range(8)}
     assert len(masks) == 64
+
+
+def test_a_drop_is_active_where_the_library_drops(lib):
+    """p * 65536 just below 1/2 rounds to 0, of which adding 1/2 makes 1."""
+    import math
+    for p in (0.5 / 65536, math.nextafter(0.5, 0) / 65536, math.nextafter(0.5, 1) / 65536, 0.0, 5e-324, 1.0):
+        d = D.Drop(p, 1)
+        args = {**NORM, "drop": d._c, "h": A[6]}       # h is x where nothing is dropped, and then refused
+        try:
+            lib.layer_norm(*args.values())
+            dropped = True
+        except D.DdpbError as e:
+            assert "pass NULL" in str(e)
+            dropped = False
+        assert d.active == dropped == (p * 65536 >= 0.5)

@@ -314,3 +314,14 @@ def test_a_drop_is_active_where_the_library_drops(lib):
             assert "pass NULL" in str(e)
             dropped = False
         assert d.active == dropped == (p * 65536 >= 0.5)
+
+
+def test_workspace_of_many_tiles_stays_in_bounds(lib):
+    """Histograms of up to 1024 counters of four bytes for 2048 keys."""
+    for n, vocab, cols in [(1 << 20, 1000, 1), (1 << 30, 1000, 1), (1 << 20, 1 << 19, 3), (1 << 24, 1000, 64),
+                           (16385, 1023, 9)]:
+        b = lib.embedding_backward_workspace_bytes(n, vocab, cols)
+        units = min(n // 8 + 1, 65536)
+        assert 16 * n <= b <= 16 * n + (n // 2048 + 1) * 4096 + units * (8 * cols + 8) + 32768 and b % 256 == 0
+    # the histogram's term is needed: 512 tiles of 1024 counters
+    assert lib.embedding_backward_workspace_bytes(1 << 20, 1000, 1) > (16 << 20) + (512 << 12)

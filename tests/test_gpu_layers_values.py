@@ -19,7 +19,8 @@ def _gpu():
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("cols", [1, 2, 3, 7, 8, 9, 20, 64, 100, 127, 256, 300, 520, 1000, 1100, 2049, 3000, 4100, 8200, 16390])
+@pytest.mark.parametrize("cols", [1, 2, 3, 7, 8, 9, 20, 64, 100, 127, 256, 300, 520, 1000, 1100, 2049, 3000, 4100, 8200,
+                                  16390])
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 def test_mean_times_rstd_beyond_fp32(cols, t):
     """(0 - mean) rstd overflows, which no column that exists computes."""

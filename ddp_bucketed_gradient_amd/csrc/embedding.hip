@@ -559,15 +559,6 @@ __global__ __launch_bounds__(256) void join_kernel(Sum a) {
   }
 }
 
-uint64_t addr(const void* p) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p)); }
-
-template <typename F>
-void by_type(int32_t dtype, F f) {
-  if (dtype == kF32) f(std::integral_constant<int, kF32>());
-  else if (dtype == kBF16) f(std::integral_constant<int, kBF16>());
-  else f(std::integral_constant<int, kF16>());
-}
-
 // The share of the zeros that launch i of `launches` writes.
 Zeros zeros_of(const LookupBackwardArgs& a, int i, int launches) {
   Zeros z = {};

@@ -1,4 +1,4 @@
-// group8.hpp -- device code that layer norm, dropout and the embedding share:
+// group8.hpp -- what the kernels of layer norm, dropout and the embedding share:
 // groups of eight consecutive elements, and the dropout's random bits.
 #pragma once
 
@@ -23,6 +23,16 @@ constexpr int kPolicyDeviceNT = 2 | 16;   // of a buffer store
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v8f __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+inline uint64_t addr(const void* p) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p)); }
+
+// f with an element type as a constant.
+template <typename F>
+void by_type(int32_t dtype, F f) {
+  if (dtype == kF32) f(std::integral_constant<int, kF32>());
+  else if (dtype == kBF16) f(std::integral_constant<int, kBF16>());
+  else f(std::integral_constant<int, kF16>());
+}
 
 template <int D> struct Of;
 template <> struct Of<kF32> { typedef float one; };

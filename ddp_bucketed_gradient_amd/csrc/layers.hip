@@ -487,8 +487,6 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(Drop a) {
   }
 }
 
-uint64_t addr(const void* p) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p)); }
-
 uint64_t bytes(int64_t stride, int32_t dtype) { return static_cast<uint64_t>(stride * dtype_size(dtype)); }
 
 unsigned grid_of(int64_t want, int64_t most) {
@@ -538,13 +536,6 @@ void launch_backward(const Backward& a, unsigned blocks, hipStream_t s) {
     go(norm_backward_kernel<D, L, K, kShifted>, T);
   });
   if (!short_row) go(norm_backward_long_kernel<D>, kLong);
-}
-
-template <typename F>
-void by_type(int32_t dtype, F f) {
-  if (dtype == kF32) f(std::integral_constant<int, kF32>());
-  else if (dtype == kBF16) f(std::integral_constant<int, kBF16>());
-  else f(std::integral_constant<int, kF16>());
 }
 
 class HipLayersDevice final : public LayersDevice {

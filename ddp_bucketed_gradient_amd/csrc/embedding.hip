@@ -68,8 +68,8 @@ __global__ __launch_bounds__(256) void lookup_kernel(Lookup a) {
 //
 //  1. Sort the places by token, stably: a radix sort, `digit` bits a pass, each
 //     a histogram of every tile of keys and a scatter; few tokens in one launch,
-//     by ranges of them. Beside it, workgroups that would
-//     be idle write the zeros of a gradient that is not added to.
+//     by ranges of them. Beside it, workgroups that would be idle write the zeros
+//     of a gradient that is not added to.
 //  2. Sum: the sorted places are cut into units of equal length, so that a
 //     token that holds many places (padding, the commonest words) is shared
 //     by many waves. A run of one token that covers no whole unit belongs to
@@ -77,8 +77,8 @@ __global__ __launch_bounds__(256) void lookup_kernel(Lookup a) {
 //     its units, and
 //  3. a last kernel adds those up.
 //
-// BERT-large (16384 tokens, 30522 x 1024 in fp32 from bf16): 42 us, of which the
-// zeros beside the sort take 26 and floor at 25 on a copy's rate.
+// BERT-large (16384 tokens, 30522 x 1024 in fp32 from bf16): 41 us, of which the
+// zeros beside the sort take 22 (5.7 TB/s), the sum 14.5 and the join 5.2.
 struct Zeros {
   uint64_t at;        // 16-byte aligned
   int64_t first, last;   // of the 16-byte pieces there, this launch's share
@@ -89,8 +89,8 @@ constexpr int kZeroBlocks = 448;                    // workgroups that write the
 constexpr int64_t kZeroPieces = kSortThreads * 8;   // that one of them writes at a time
 
 // Non-temporal stores of device scope: BERT-large's 125 MB of zeros beside the
-// sort take 26 us instead of 36, and the sum that follows, whose reads would meet
-// the caches full of them, 12.5 us instead of 22.6.
+// sort take 22.2 us instead of 31.9, and the sum that follows, whose reads would
+// meet the caches full of them, 14.6 us instead of 22.8.
 __device__ __forceinline__ void write_zeros(const Zeros& z, uint32_t block, uint32_t blocks) {
   for (int64_t from = z.first + block * kZeroPieces; from < z.last; from += blocks * kZeroPieces) {
     const uint64_t base = z.at + static_cast<uint64_t>(from) * 16;
@@ -206,6 +206,17 @@ __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* waves) {
 // What it counts of the ranges before its own is where its places begin. The
 // order is one of groups: t % kRanges, then t. Bound by latency: 8192 tokens take
 // 10.5 us, where two passes of count and scatter took 24.
+//
+// 16384 tokens, because their LDS (132 KB) is the largest that holds a power of two
+// of them. The whole added-to gradient of 64 columns, by ranges and by tiles, which
+// sort in two passes (30522 rows) or in one (1000 rows):
+//   tokens  30522 rows: ranges, tiles   1000 rows: ranges, tiles
+//     1024        17.2, 23.5 us              15.2, 18.5 us
+//     8192        23.0, 29.3                 20.9, 22.0
+//    16384        32.8, 36.2                 28.5, 25.7
+//    16385        39.1, 42.9                 33.0, 29.7
+// and BERT-large's 30522 x 1024 written: 16384 tokens 39.4, 49.7, 16385 tokens 50.8,
+// 56.7 (ranges of up to 18432 tokens built for this comparison).
 constexpr int kRangeBits = 6, kDigits = 1 << kRangeBits;
 struct RangeLds {
   uint32_t token[kRangeKeys];
@@ -412,11 +423,11 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t x, int i) {
 // the rows themselves is uniform. The rows of kAhead places are loaded together,
 // with what stands in the table where the sums are added to that.
 //
-// BERT-large's 16384 places in bf16 into fp32: 14.4 us behind the zeros (3.4 TB/s of
+// BERT-large's 16384 places in bf16 into fp32: 14.5 us behind the zeros (3.4 TB/s of
 // rows in and out; four waves a CU, of which each goes through the latencies of
 // keys, rows and stores once). 131072 places of 768 columns, 40 % of them one
-// token, added to: 77 us, 3.6 TB/s of scattered rows in and out (the rows of dy
-// alone: 41 us, 4.4 TB/s). Twice or four times the waves took 69-78 us (and the
+// token, added to: 77 us for 257 MB of scattered rows in and out, 3.3 TB/s (3.6 of
+// the bytes that counters see; the rows of dy alone: 41 us, 4.4 TB/s). Twice or four times the waves took 69-78 us (and the
 // join twice as long), finished rows collected in LDS and written eight at a
 // time 84, old rows loaded only when a run ends 89.
 template <int D, int GD, bool ADD, int EDGE>

@@ -449,8 +449,9 @@ __global__ __launch_bounds__(kWeightCols * kWeightWaves) void norm_weights_kerne
 
 // ---------------------------------------------------------------------------
 // Dropout, with or without a residual: a group of eight elements to a lane,
-// counted row by row. Bound by HBM: 8192 x 8192 in bf16 45 us, 6.0 TB/s (with two
-// or four groups to a lane 46 and 48).
+// counted row by row. Bound by HBM: 8192 x 8192 in bf16 45.4 us, 5.9 TB/s (with
+// two or four groups to a lane, measured in turn, 46.2 and 48.4; 2048 x 1024: 2.96,
+// 2.84 and 3.50).
 struct Drop {
   uint64_t x, residual, y;
   int64_t x_stride, residual_stride;   // in elements

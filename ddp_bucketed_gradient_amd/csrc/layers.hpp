@@ -100,6 +100,25 @@ struct LookupBackwardArgs {
 // How a layer norm is cut: lanes of a row, groups of each lane. Rows up to 1024
 // elements stay in one wave (no barrier), longer ones in a workgroup; a row that
 // no shape holds in registers is read again for each of its passes (lanes = 0).
+// The smallest shape that holds a row, against the next one, at and behind each
+// border, in bf16 with 2^25 elements: the norm with a residual, its backward pass
+// with the weights' gradients (us):
+//     cols      taken              next
+//      128   16 x 1   41,  37   64 x 1    75, 119
+//      136   64 x 1   71, 115   64 x 2    91, 124
+//      512   64 x 1   41,  41   64 x 2    43,  43
+//      520   64 x 2   48,  50   256 x 1   61, 132
+//     1024   64 x 2   42,  38   256 x 1   42,  73
+//     1032   256 x 1  44,  74   256 x 2   56,  81
+//     2048   256 x 1  41,  49   256 x 2   42,  53
+//     2056   256 x 2  51,  58   512 x 2   60,  83
+//     4096   256 x 2  42,  50   512 x 2   44,  55
+//     4104   512 x 2  52,  58   1024 x 2  69,  85
+//     8192   512 x 2  41,  53   1024 x 2  52,  69
+//     8200   1024 x 2 54,  74   none      79, 473
+//    16384   1024 x 2 42,  75   none      61, 257
+// In fp32 (2^24 elements) the same are ahead, but for 1024 columns (forward 49, next
+// 46), 2056 (52, 44) and 4096 (forward 47, 45; backward 45, 39).
 struct NormShape {
   int lanes, groups;
 };

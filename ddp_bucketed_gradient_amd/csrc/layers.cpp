@@ -112,8 +112,9 @@ int64_t norm_backward_workspace(int64_t rows, int64_t cols) {
 
 int check(const NormForwardArgs& a, std::string* err) {
   const char* what = "layer_norm";
-  const int64_t size = dtype_size(a.dtype), n = a.rows * a.cols;
+  const int64_t size = dtype_size(a.dtype);
   if (!norm_sizes_ok(a.rows, a.cols)) return fail(err, what, "rows must be in 0..2^31 - 1, cols in 1..2^20");
+  const int64_t n = a.rows * a.cols;
   if (!(a.eps >= 0.0) || !std::isfinite(static_cast<float>(a.eps))) return fail(err, what, "eps must be finite and not negative");
   if (!matrix_ok(a.x, a.rows, size, true) || !matrix_ok(a.residual, a.rows, size, false))
     return fail(err, what, "NULL, misaligned or too widely spread input");

@@ -325,3 +325,15 @@ def test_workspace_of_many_tiles_stays_in_bounds(lib):
         assert 16 * n <= b <= 16 * n + (n // 2048 + 1) * 4096 + units * (8 * cols + 8) + 32768 and b % 256 == 0
     # the histogram's term is needed: 512 tiles of 1024 counters
     assert lib.embedding_backward_workspace_bytes(1 << 20, 1000, 1) > (16 << 20) + (512 << 12)
+
+
+@pytest.mark.parametrize("rows, cols", [(1 << 62, 4), (4, 1 << 62), ((1 << 63) - 1, (1 << 63) - 1), (-(1 << 63), 2)])
+def test_sizes_whose_product_does_not_fit_are_refused(lib, rows, cols):
+    for name in ("layer_norm", "layer_norm_backward", "dropout"):
+        with pytest.raises(D.DdpbError) as e:
+            getattr(lib, name)(*{**CALLS[name], "rows": rows, "cols": cols}.values())
+        assert e.value.code == D.E_ARG
+    for name in ("embedding", "embedding_backward"):
+        with pytest.raises(D.DdpbError) as e:
+            getattr(lib, name)(*{**CALLS[name], "n": rows, "cols": cols}.values())
+        assert e.value.code == D.E_ARG
